@@ -119,7 +119,12 @@ extern "C" {
 #define NF4_PATH_GROUPED_BWD    7  /* grouped (expert) input gradient           */
 #define NF4_PATH_FWD_8BIT       8  /* 8-bit blockwise forward (plain or grouped) */
 #define NF4_PATH_BWD_8BIT       9  /* 8-bit blockwise input gradient            */
-#define NF4_PATH_COUNT         10
+#define NF4_PATH_KV_APPEND     10  /* attention (nf4_attn.h): cache append      */
+#define NF4_PATH_KV_DEQUANTIZE 11  /* cache read back                           */
+#define NF4_PATH_KV_ATTENTION  12  /* attention over the 4-bit cache            */
+#define NF4_PATH_PROMPT_FWD    13  /* causal attention over packed prompts      */
+#define NF4_PATH_PROMPT_BWD    14  /* its backward pass                         */
+#define NF4_PATH_COUNT         15
 
 /*
  * nf4_quantize -- NF4 blockwise quantisation of w [N, K] (bitsandbytes #2034,

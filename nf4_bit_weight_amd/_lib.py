@@ -1,4 +1,5 @@
-"""ctypes loader for libnf4.so (the C ABI declared in include/nf4.h).
+"""ctypes loader for libnf4.so (the C ABI declared in include/nf4.h and
+include/nf4_attn.h).
 
 The library must be built in-tree first (`python -m nf4_bit_weight_amd.build`
 or __graft_entry__.build()).  There is no fallback: if the shared library is
@@ -38,7 +39,8 @@ NF4_OP_MATMUL_FWD_8BIT = 5
 NF4_OP_MATMUL_BWD_INPUT_8BIT = 6
 
 PATHS = ("quantize", "dequantize", "fwd_tiled", "fwd_small_m", "bwd_tiled",
-         "splitk_reduce", "grouped_fwd", "grouped_bwd", "fwd_8bit", "bwd_8bit")
+         "splitk_reduce", "grouped_fwd", "grouped_bwd", "fwd_8bit", "bwd_8bit",
+         "kv_append", "kv_dequantize", "kv_attention", "prompt_fwd", "prompt_bwd")
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -48,7 +50,11 @@ _size = ctypes.c_size_t
 
 _W = [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64]   # packed .. nested_code256, N, K
 
-# name -> (restype, argtypes); the full exported surface of nf4.h
+_f32 = ctypes.c_float
+_CACHE = [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32]   # k_codes .. v_scale, P, page, Hkv, D
+_SEQS = [_vp, _vp, _i32, _vp, _i32]                     # offsets, lengths, B, page_table, width
+
+# name -> (restype, argtypes); the full exported surface of nf4.h and nf4_attn.h
 SIGNATURES = {
     "nf4_quantize": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _size, _vp]),
     "nf4_dequantize": (_int, [*_W, _int, _vp, _vp]),
@@ -71,6 +77,16 @@ SIGNATURES = {
     "nf4_reset_path_counts": (None, []),
     "nf4_status_str": (ctypes.c_char_p, [_int]),
     "nf4_version": (ctypes.c_char_p, []),
+    "nf4_kv_append": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, *_SEQS, _vp, _i32, _int, *_CACHE,
+                             _vp, _vp, _int, _vp]),
+    "nf4_kv_dequantize": (_int, [_i64, *_SEQS, *_CACHE, _vp, _vp, _int, _vp]),
+    "nf4_kv_attention": (_int, [_vp, _i64, _i64, _i32, *_SEQS, *_CACHE, _f32, _vp, _int, _vp, _size, _vp]),
+    "nf4_kv_attention_workspace": (_size, [_i64, _i32, _i32, _i32, _i32]),
+    "nf4_prompt_attention_fwd": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i32, _i32, _i32, _i32, _f32,
+                                        _vp, _vp, _int, _vp]),
+    "nf4_prompt_attention_bwd": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i32, _i32,
+                                        _i32, _i32, _f32, _vp, _vp, _vp, _int, _vp, _size, _vp]),
+    "nf4_prompt_attention_bwd_workspace": (_size, [_i64, _i32]),
 }
 
 _lib = None

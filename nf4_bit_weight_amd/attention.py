@@ -1,0 +1,326 @@
+"""Attention between the quantised projections: a paged key/value cache held in
+4 bits, attention over it, and causal attention over packed prompts (the C ABI
+of include/nf4_attn.h).
+
+As in `api`, argument marshalling only: tensors are checked, their pointers and
+the current stream of their device are passed on, and a non-zero status raises
+NF4Error.
+
+Tensor conventions (all on one CUDA/HIP device):
+  q               bfloat16 [T, Hq, D]; k, v  bfloat16 [T, Hkv, D]; D is 64 or 128
+                  and Hq a multiple of Hkv.  The heads of a row are contiguous;
+                  the rows may be strided (a slice of a joint projection), by a
+                  multiple of 8 elements
+  offsets         int32 [B + 1], rows offsets[b] .. offsets[b+1]-1 belong to
+                  sequence b; for the cache calls None means one row each
+  lengths         int32 [B], tokens of each sequence with the rows of the call
+  page_table      int32 [B, width], the pages that hold a sequence's tokens
+Rows outside every sequence are zeros in a result allocated here and left as
+they were in one that is passed in.
+"""
+
+from __future__ import annotations
+
+import math
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import _lib as L
+from .api import _need, _ptr
+
+_BLOCK = 64
+
+
+@dataclass
+class NF4KVCache:
+    """A paged key/value cache held in 4 bits (layout and encoding in
+    nf4_attn.h): every vector of D elements is D/2 bytes of fp4 (e2m1) patterns
+    and one fp32 scale per 64 elements."""
+    k_codes: torch.Tensor      # uint8   [P, Hkv, page, D / 2]
+    k_scale: torch.Tensor      # float32 [P, Hkv, page, D / 64]
+    v_codes: torch.Tensor
+    v_scale: torch.Tensor
+
+    @property
+    def pages(self) -> int:
+        return self.k_codes.shape[0]
+
+    @property
+    def kv_heads(self) -> int:
+        return self.k_codes.shape[1]
+
+    @property
+    def page_size(self) -> int:
+        return self.k_codes.shape[2]
+
+    @property
+    def head_dim(self) -> int:
+        return 2 * self.k_codes.shape[3]
+
+    def tensors(self):
+        return self.k_codes, self.k_scale, self.v_codes, self.v_scale
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in self.tensors())
+
+
+def nf4_kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda") -> NF4KVCache:
+    """An empty cache (zeros) of `pages` pages of `page_size` tokens."""
+    if head_dim not in (64, 128):
+        raise ValueError(f"head_dim must be 64 or 128, got {head_dim}")
+    if page_size < 16 or page_size % 16:
+        raise ValueError(f"page_size must be a multiple of 16, got {page_size}")
+    if pages < 0 or kv_heads < 1:
+        raise ValueError("pages must be at least 0 and kv_heads at least 1")
+    shape = (pages, kv_heads, page_size)
+    codes = [torch.zeros((*shape, head_dim // 2), dtype=torch.uint8, device=device) for _ in range(2)]
+    scale = [torch.zeros((*shape, head_dim // _BLOCK), dtype=torch.float32, device=device) for _ in range(2)]
+    return NF4KVCache(codes[0], scale[0], codes[1], scale[1])
+
+
+def _cache_args(c: NF4KVCache):
+    if c.k_codes.dim() != 4:
+        raise ValueError("k_codes must be [pages, kv_heads, page, head_dim / 2]")
+    P, H, page, half = c.k_codes.shape
+    if half not in (32, 64):
+        raise ValueError(f"the cache's head_dim must be 64 or 128, got {2 * half}")
+    if page < 16 or page % 16:
+        raise ValueError(f"the cache's page must be a multiple of 16 tokens, got {page}")
+    dev, n = c.k_codes.device, P * H * page
+    _need(c.k_codes, "k_codes", torch.uint8)
+    _need(c.v_codes, "v_codes", torch.uint8, n * half, dev)
+    _need(c.k_scale, "k_scale", torch.float32, n * half // 32, dev)
+    _need(c.v_scale, "v_scale", torch.float32, n * half // 32, dev)
+    return (*(t.data_ptr() for t in c.tensors()), P, page, H, 2 * half)
+
+
+def _seq_args(rows: int, lengths, page_table, offsets, device):
+    _need(lengths, "lengths", torch.int32, device=device)
+    if page_table.dim() != 2 or lengths.dim() != 1 or page_table.shape[0] != lengths.shape[0]:
+        raise ValueError("lengths must be [B] and page_table [B, width]")
+    B = lengths.shape[0]
+    _need(page_table, "page_table", torch.int32, device=device)
+    if offsets is None:
+        if rows != B:
+            raise ValueError(f"without offsets there is one row per sequence: {rows} rows, {B} sequences")
+    else:
+        _need(offsets, "offsets", torch.int32, B + 1, device)
+    return _ptr(offsets), lengths.data_ptr(), B, page_table.data_ptr(), page_table.shape[1]
+
+
+def _rows(t: torch.Tensor, name: str, heads: Optional[int], D: int, device, rows: Optional[int] = None) -> int:
+    """Check a [T, heads, D] bf16 tensor with free row stride; its stride."""
+    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [T, {'heads' if heads is None else heads}, {D}], got {tuple(t.shape)}")
+    if rows is not None and t.shape[0] != rows:
+        raise ValueError(f"{name} has {t.shape[0]} rows, expected {rows}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    T, H, _ = t.shape
+    if T * H == 0:
+        return 0
+    sr, sh, sd = t.stride()
+    if sd != 1 or (H > 1 and sh != D) or (T > 1 and sr % 8):
+        raise ValueError(f"{name}: the heads of a row must be contiguous and rows a multiple of 8 elements apart")
+    return sr if T > 1 else 0
+
+
+def _result(t: Optional[torch.Tensor], name: str, shape, device):
+    """(result tensor, whether rows outside every sequence are to be filled)."""
+    if t is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device), 1
+    _need(t, name, torch.bfloat16, math.prod(shape), device)
+    return t, 0
+
+
+class _on:
+    """The device of the tensors made current for a launch, if it is not."""
+
+    __slots__ = ("guard",)
+
+    def __init__(self, device):
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _scale(scale: Optional[float], D: int) -> float:
+    s = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    if not (s > 0 and math.isfinite(s)):
+        raise ValueError(f"scale must be positive and finite, got {scale}")
+    return s
+
+
+def nf4_kv_append(cache: NF4KVCache, k: torch.Tensor, v: torch.Tensor, lengths: torch.Tensor,
+                  page_table: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                  inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False,
+                  q: Optional[torch.Tensor] = None, return_k: bool = False,
+                  q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+    """Put new keys and values into the cache, keys turned by their positions
+    (inv_freq float32 [rotary / 2]; pairs (i, i + rotary / 2), or neighbours with
+    `interleaved`).  Returns (q turned alike or None, the turned bf16 keys with
+    `return_k` or None)."""
+    cargs = _cache_args(cache)
+    H, D, dev = cargs[6], cargs[7], cache.k_codes.device
+    ks = _rows(k, "k", H, D, dev)
+    T = k.shape[0]
+    vs = _rows(v, "v", H, D, dev, T)
+    sargs = _seq_args(T, lengths, page_table, offsets, dev)
+    rotary = 0
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", torch.float32, device=dev)
+        rotary = 2 * inv_freq.numel()
+        if rotary > D or rotary % 16:
+            raise ValueError(f"inv_freq must have a multiple of 8 elements, at most {D // 2}, got {inv_freq.numel()}")
+    Hq, qs, fill = H, 0, 1
+    if q is not None:
+        qs = _rows(q, "q", None, D, dev, T)
+        Hq = q.shape[1]
+        if Hq < 1 or Hq % H:
+            raise ValueError(f"{Hq} query heads do not divide over {H} key heads")
+        q_out, fill = _result(q_out, "q_out", (T, Hq, D), dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k_out is not None or return_k:
+        k_out, kfill = _result(k_out, "k_out", (T, H, D), dev)
+        if q is not None and kfill != fill:
+            raise ValueError("pass both of q_out and k_out, or neither")
+        fill = kfill
+    with _on(dev) as stream:
+        st = L.lib().nf4_kv_append(_ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, *sargs, _ptr(inv_freq), rotary,
+                                   int(interleaved), *cargs, _ptr(q_out), _ptr(k_out), fill, stream)
+    L.check("nf4_kv_append", st)
+    return q_out, k_out
+
+
+def nf4_kv_dequantize(cache: NF4KVCache, lengths: torch.Tensor, page_table: torch.Tensor,
+                      offsets: Optional[torch.Tensor] = None, rows: Optional[int] = None,
+                      k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None):
+    """The keys and values that the cache stands for, bf16 [rows, Hkv, D]: of the
+    last offsets[b+1] - offsets[b] tokens of each sequence (without offsets, the
+    last one).  `rows` is the number of rows of the result."""
+    cargs = _cache_args(cache)
+    H, D, dev = cargs[6], cargs[7], cache.k_codes.device
+    if rows is None:
+        if offsets is not None:
+            raise ValueError("with offsets, pass the number of rows")
+        rows = lengths.shape[0]
+    if rows < 0:
+        raise ValueError(f"rows must not be negative, got {rows}")
+    sargs = _seq_args(rows, lengths, page_table, offsets, dev)
+    if (k_out is None) != (v_out is None):
+        raise ValueError("pass both of k_out and v_out, or neither")
+    k_out, fill = _result(k_out, "k_out", (rows, H, D), dev)
+    v_out, _ = _result(v_out, "v_out", (rows, H, D), dev)
+    with _on(dev) as stream:
+        st = L.lib().nf4_kv_dequantize(rows, *sargs, *cargs, k_out.data_ptr(), v_out.data_ptr(), fill, stream)
+    L.check("nf4_kv_dequantize", st)
+    return k_out, v_out
+
+
+def nf4_kv_attention_workspace(T: int, B: int, Hq: int, Hkv: int, D: int) -> int:
+    n = int(L.lib().nf4_kv_attention_workspace(T, B, Hq, Hkv, D))
+    if n == 2 ** 64 - 1:
+        raise ValueError(f"unsupported sizes: T {T}, B {B}, heads {Hq} on {Hkv}, D {D}")
+    return n
+
+
+def nf4_kv_attention(q: torch.Tensor, cache: NF4KVCache, lengths: torch.Tensor, page_table: torch.Tensor,
+                     offsets: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of the newest rows of each sequence over its cached tokens, each
+    row seeing the tokens up to its own (scale 1/sqrt(D) unless given)."""
+    cargs = _cache_args(cache)
+    H, D, dev = cargs[6], cargs[7], cache.k_codes.device
+    qs = _rows(q, "q", None, D, dev)
+    T, Hq = q.shape[0], q.shape[1]
+    if Hq < 1 or Hq % H:
+        raise ValueError(f"{Hq} query heads do not divide over {H} key heads")
+    sargs = _seq_args(T, lengths, page_table, offsets, dev)
+    s = _scale(scale, D)
+    out, fill = _result(out, "out", (T, Hq, D), dev)
+    with _on(dev) as stream:
+        need = nf4_kv_attention_workspace(T, sargs[2], Hq, H, D)
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _need(ws, "ws", device=dev)
+        st = L.lib().nf4_kv_attention(q.data_ptr(), qs, T, Hq, *sargs, *cargs, s, out.data_ptr(), fill, ws.data_ptr(),
+                                      ws.numel() * ws.element_size(), stream)
+    L.check("nf4_kv_attention", st)
+    return out
+
+
+def _prompt_args(q, k, v, offsets):
+    D = q.shape[2] if q.dim() == 3 else 0
+    if D not in (64, 128):
+        raise ValueError(f"q must be [T, Hq, D] with D 64 or 128, got {tuple(q.shape)}")
+    dev = q.device
+    qs = _rows(q, "q", None, D, dev)
+    T, Hq = q.shape[0], q.shape[1]
+    ks = _rows(k, "k", None, D, dev, T)
+    H = k.shape[1]
+    vs = _rows(v, "v", H, D, dev, T)
+    if H < 1 or Hq < 1 or Hq % H:
+        raise ValueError(f"{Hq} query heads do not divide over {H} key heads")
+    _need(offsets, "offsets", torch.int32, device=dev)
+    if offsets.dim() != 1 or offsets.numel() < 1:
+        raise ValueError("offsets must be [B + 1]")
+    return dev, T, offsets.numel() - 1, Hq, H, D, (q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs)
+
+
+def nf4_prompt_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor,
+                             scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                             lse: Optional[torch.Tensor] = None, want_lse: bool = False):
+    """Causal attention inside each packed sequence; (out, lse or None).  lse
+    float32 [Hq, T] is what the backward call needs beside out."""
+    dev, T, B, Hq, H, D, ptrs = _prompt_args(q, k, v, offsets)
+    s = _scale(scale, D)
+    out, fill = _result(out, "out", (T, Hq, D), dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, T * Hq, dev)
+    elif want_lse:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+    with _on(dev) as stream:
+        st = L.lib().nf4_prompt_attention_fwd(*ptrs, T, offsets.data_ptr(), B, Hq, H, D, s, out.data_ptr(), _ptr(lse),
+                                              fill, stream)
+    L.check("nf4_prompt_attention_fwd", st)
+    return out, lse
+
+
+def nf4_prompt_attention_bwd(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                             out: torch.Tensor, lse: torch.Tensor, offsets: torch.Tensor,
+                             scale: Optional[float] = None, ws: Optional[torch.Tensor] = None):
+    """(grad_q, grad_k, grad_v) from the forward call's inputs, out and lse."""
+    dev, T, B, Hq, H, D, ptrs = _prompt_args(q, k, v, offsets)
+    s = _scale(scale, D)
+    gs = _rows(grad_out, "grad_out", Hq, D, dev, T)
+    _need(out, "out", torch.bfloat16, T * Hq * D, dev)
+    _need(lse, "lse", torch.float32, T * Hq, dev)
+    gq = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    gk = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+    gv = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+    with _on(dev) as stream:
+        if ws is None:
+            need = int(L.lib().nf4_prompt_attention_bwd_workspace(T, Hq))
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _need(ws, "ws", device=dev)
+        st = L.lib().nf4_prompt_attention_bwd(grad_out.data_ptr(), gs, *ptrs, out.data_ptr(), lse.data_ptr(), T,
+                                              offsets.data_ptr(), B, Hq, H, D, s, gq.data_ptr(), gk.data_ptr(),
+                                              gv.data_ptr(), 1, ws.data_ptr(), ws.numel() * ws.element_size(), stream)
+    L.check("nf4_prompt_attention_bwd", st)
+    return gq, gk, gv

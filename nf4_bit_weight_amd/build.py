@@ -19,7 +19,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libnf4.so")
 ARCH = "gfx950"
 
-SOURCES = ("nf4_abi.hip", "nf4_codec.hip", "nf4_gemm.hip", "nf4_gemv.hip")
+SOURCES = ("nf4_abi.hip", "nf4_codec.hip", "nf4_gemm.hip", "nf4_gemv.hip", "nf4_attn_abi.hip",
+           "nf4_kv.hip", "nf4_prompt.hip")
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",

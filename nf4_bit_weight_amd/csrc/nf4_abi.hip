@@ -392,7 +392,7 @@ const char* nf4_status_str(int status) {
     case NF4_OK: return "NF4_OK: success";
     case NF4_ERR_NULL: return "NF4_ERR_NULL: a required pointer is NULL";
     case NF4_ERR_SHAPE: return "NF4_ERR_SHAPE: invalid sizes";
-    case NF4_ERR_UNSUPPORTED: return "NF4_ERR_UNSUPPORTED: unsupported shape (K % 64, N % 8 or size limit)";
+    case NF4_ERR_UNSUPPORTED: return "NF4_ERR_UNSUPPORTED: unsupported shape (K % 64, N % 8, head or page size, size limit)";
     case NF4_ERR_ALIGN: return "NF4_ERR_ALIGN: a pointer is not 16-byte aligned";
     case NF4_ERR_WORKSPACE: return "NF4_ERR_WORKSPACE: workspace missing or too small";
     case NF4_ERR_HIP: return "NF4_ERR_HIP: the HIP runtime reported an error";

@@ -1,0 +1,148 @@
+// Launch interface and device helpers of the attention kernels (nf4_kv.hip,
+// nf4_prompt.hip), between the C ABI of nf4_attn.h and the kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "nf4_device.hpp"
+
+namespace nf4 {
+
+// Paged 4-bit cache (layout in nf4_attn.h).
+struct KVCache {
+  uint8_t* k_codes;
+  float* k_scale;
+  uint8_t* v_codes;
+  float* v_scale;
+  int64_t P;
+  int32_t page, Hkv, D;
+};
+
+// Which rows belong to which sequence, and where the sequence's tokens lie.
+struct KVSeqs {
+  const int32_t* offsets;   // NULL: one row per sequence
+  const int32_t* lengths;
+  const int32_t* table;
+  int32_t B, width;
+  int32_t T;
+};
+
+struct AppendArgs {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  uint16_t *q_out, *k_out;
+  const float* inv_freq;
+  int32_t Hq, half;         // rotary / 2
+  int interleaved, fill;
+};
+
+struct PromptArgs {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t* offsets;
+  int32_t T, B, Hq, Hkv, D;
+  float scale;
+  int fill;
+};
+
+hipError_t launch_kv_append(const KVCache& c, const KVSeqs& s, const AppendArgs& a, hipStream_t stream);
+hipError_t launch_kv_dequantize(const KVCache& c, const KVSeqs& s, void* k_out, void* v_out, int fill,
+                                hipStream_t stream);
+
+// How a cache attention call is cut: `workers` workgroups share the steps of
+// all (sequence, row tile, key head) units evenly; a unit that several of them
+// share is joined from their partial results by a second kernel.
+struct KVAttnPlan {
+  int mt;          // row tiles of 16 (query row, head) rows per unit
+  int workers;
+  size_t ws_bytes;
+};
+KVAttnPlan plan_kv_attention(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int cus);
+hipError_t launch_kv_attention(const KVAttnPlan& pl, const KVCache& c, const KVSeqs& s, const void* q,
+                               int64_t q_stride, int32_t Hq, float scale, void* out, int fill, void* ws,
+                               hipStream_t stream);
+
+hipError_t launch_prompt_fwd(const PromptArgs& a, void* out, float* lse, hipStream_t stream);
+hipError_t launch_prompt_bwd(const PromptArgs& a, const void* grad_out, int64_t grad_stride, const void* out,
+                             const float* lse, void* grad_q, void* grad_k, void* grad_v, void* ws,
+                             hipStream_t stream);
+
+// ---- device helpers ----------------------------------------------------------
+
+__device__ __forceinline__ int wave_sum(int x) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
+  return x;
+}
+
+// Inclusive prefix sum over the wave.
+__device__ __forceinline__ int wave_scan(int x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// x of this lane and of the lane whose number differs in bit 5 (bit 4).  In
+// assembly: compiled from the builtin, both results came out as the first.
+// The swap needs two wait states behind the write of its operands.
+__device__ __forceinline__ f32x2_t swap32(float x) {
+  float y = x;
+  asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+  return f32x2_t{x, y};
+}
+__device__ __forceinline__ f32x2_t swap16(float x) {
+  float y = x;
+  asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+  return f32x2_t{x, y};
+}
+
+// max / sum over the two lanes that hold one row of a 32-wide tile
+__device__ __forceinline__ float half_max(float x) {
+  const f32x2_t a = swap32(x);
+  return fmaxf(a[0], a[1]);
+}
+__device__ __forceinline__ float half_sum(float x) {
+  const f32x2_t a = swap32(x);
+  return a[0] + a[1];
+}
+// and over the four lanes that hold one row of a 16-wide tile
+__device__ __forceinline__ float quad_max(float x) {
+  const f32x2_t a = swap16(half_max(x));
+  return fmaxf(a[0], a[1]);
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  const f32x2_t a = swap16(half_sum(x));
+  return a[0] + a[1];
+}
+
+// The rows of sequence b, clamped into 0 .. T whatever the offsets hold.
+__device__ __forceinline__ void seq_rows(const int32_t* offsets, int b, int T, int& first, int& n) {
+  if (!offsets) {
+    first = b;
+    n = b < T ? 1 : 0;
+    return;
+  }
+  const int s = min(max(offsets[b], 0), T), e = min(max(offsets[b + 1], s), T);
+  first = s;
+  n = e - s;
+}
+
+// The sequence that row t belongs to, or -1 (all lanes of the wave take part
+// and t is the same in all of them): the last b with offsets[b] <= t.
+__device__ __forceinline__ int seq_of(const int32_t* offsets, int B, int T, int t) {
+  if (!offsets) return t < B ? t : -1;
+  int count = 0;
+  for (int i = threadIdx.x & 63; i - (int)(threadIdx.x & 63) <= B; i += 64)
+    count += __popcll(__ballot(i <= B && offsets[min(i, B)] <= t));
+  const int b = count - 1;
+  return (b >= 0 && b < B && t < offsets[b + 1]) ? b : -1;
+}
+
+}  // namespace nf4
