@@ -14,8 +14,8 @@
  *
  * Heads.  q rows are bf16 [T, Hq, D], k and v rows bf16 [T, Hkv, D], D = 64 or
  * 128, Hq a multiple of Hkv; query head i reads key head i / (Hq / Hkv).
- * *_stride is the distance between rows in elements (a multiple of 8; the
- * heads of one row are contiguous), so slices of a joint projection are taken
+ * *_stride is the distance between rows in elements (a multiple of 8, at most
+ * 2^24; the heads of one row are contiguous), so slices of a joint projection are taken
  * as they are.  All row pointers are 16-byte aligned.  Written tensors are
  * contiguous.
  *
@@ -113,34 +113,38 @@ size_t nf4_kv_attention_workspace(int64_t T, int32_t B, int32_t Hq, int32_t Hkv,
 /*
  * nf4_prompt_attention_fwd -- causal attention inside each packed sequence:
  * out[t, i] = sum over s <= t of t's sequence of softmax_s(scale q[t, i] .
- * k[s, h]) v[s, h].  out bf16 [T, Hq, D].  lse f32 [Hq, T]: the natural
- * logarithm of each row's sum of exponentials, kept for the backward pass;
- * NULL if not wanted.  bf16 products with fp32 sums; the softmax is fp32, its
+ * k[s, h]) v[s, h].  out bf16 [T, Hq, D].  For the backward pass, NULL if not
+ * wanted: lse f32 [Hq, T], the natural logarithm of each row's sum of
+ * exponentials, and out_rest bf16 [T, Hq, D], what the rounding of out took
+ * away.  bf16 products with fp32 sums; the softmax is fp32, its
  * weights are rounded once to bf16.
  */
 int nf4_prompt_attention_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                              const void* v, int64_t v_stride, int64_t T,
                              const int32_t* offsets, int32_t B, int32_t Hq, int32_t Hkv,
-                             int32_t D, float scale, void* out, float* lse,
-                             int fill_outside, void* stream);
+                             int32_t D, float scale, void* out, void* out_rest,
+                             float* lse, int fill_outside, void* stream);
 
 /*
  * nf4_prompt_attention_bwd -- grad_q bf16 [T, Hq, D], grad_k and grad_v bf16
  * [T, Hkv, D] (summed over the query heads that share a key head) from
- * grad_out bf16 (row stride grad_stride), the inputs, and out and lse of the
- * forward call.
- *   ws  nf4_prompt_attention_bwd_workspace(T, Hq) bytes, 16-byte aligned
+ * grad_out bf16 (row stride grad_stride), the inputs, and out, out_rest and lse of
+ * the forward call.  Without out_rest (NULL) grad_out . out is taken from the
+ * rounded output, which adds its rounding to grad_q and grad_k.
+ *   ws  nf4_prompt_attention_bwd_workspace(...) bytes, 16-byte aligned
  */
 int nf4_prompt_attention_bwd(const void* grad_out, int64_t grad_stride,
                              const void* q, int64_t q_stride, const void* k, int64_t k_stride,
-                             const void* v, int64_t v_stride, const void* out, const float* lse,
+                             const void* v, int64_t v_stride, const void* out,
+                             const void* out_rest, const float* lse,
                              int64_t T, const int32_t* offsets, int32_t B, int32_t Hq,
                              int32_t Hkv, int32_t D, float scale,
                              void* grad_q, void* grad_k, void* grad_v,
                              int fill_outside, void* ws, size_t ws_bytes, void* stream);
 
-/* Workspace bytes of nf4_prompt_attention_bwd; SIZE_MAX for invalid sizes. */
-size_t nf4_prompt_attention_bwd_workspace(int64_t T, int32_t Hq);
+/* Workspace bytes of nf4_prompt_attention_bwd for these sizes on the current
+ * device; SIZE_MAX for sizes it refuses. */
+size_t nf4_prompt_attention_bwd_workspace(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D);
 
 #ifdef __cplusplus
 }  /* extern "C" */

@@ -140,17 +140,19 @@ def _result(t: Optional[torch.Tensor], name: str, shape, device):
 
 
 class _on:
-    """The device of the tensors made current for a launch, if it is not."""
+    """The device of the tensors made current for a launch, if it is not, and
+    the handle of its current stream."""
 
-    __slots__ = ("guard",)
+    __slots__ = ("index", "guard")
 
     def __init__(self, device):
+        self.index = device.index
         self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         if self.guard is not None:
@@ -283,44 +285,46 @@ def _prompt_args(q, k, v, offsets):
 
 
 def nf4_prompt_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor,
-                             scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-                             lse: Optional[torch.Tensor] = None, want_lse: bool = False):
-    """Causal attention inside each packed sequence; (out, lse or None).  lse
-    float32 [Hq, T] is what the backward call needs beside out."""
+                             scale: Optional[float] = None, out: Optional[torch.Tensor] = None, for_backward: bool = False):
+    """Causal attention inside each packed sequence.  Returns out, or with
+    for_backward what the backward call takes: (out, out_rest, lse), out_rest
+    bf16 like out and lse float32 [Hq, T]."""
     dev, T, B, Hq, H, D, ptrs = _prompt_args(q, k, v, offsets)
     s = _scale(scale, D)
     out, fill = _result(out, "out", (T, Hq, D), dev)
-    if lse is not None:
-        _need(lse, "lse", torch.float32, T * Hq, dev)
-    elif want_lse:
+    rest = lse = None
+    if for_backward:
+        rest = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
         lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
     with _on(dev) as stream:
-        st = L.lib().nf4_prompt_attention_fwd(*ptrs, T, offsets.data_ptr(), B, Hq, H, D, s, out.data_ptr(), _ptr(lse),
-                                              fill, stream)
+        st = L.lib().nf4_prompt_attention_fwd(*ptrs, T, offsets.data_ptr(), B, Hq, H, D, s, out.data_ptr(), _ptr(rest),
+                                              _ptr(lse), fill, stream)
     L.check("nf4_prompt_attention_fwd", st)
-    return out, lse
+    return (out, rest, lse) if for_backward else out
 
 
 def nf4_prompt_attention_bwd(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
-                             out: torch.Tensor, lse: torch.Tensor, offsets: torch.Tensor,
-                             scale: Optional[float] = None, ws: Optional[torch.Tensor] = None):
-    """(grad_q, grad_k, grad_v) from the forward call's inputs, out and lse."""
+                             out: torch.Tensor, out_rest: Optional[torch.Tensor], lse: torch.Tensor,
+                             offsets: torch.Tensor, scale: Optional[float] = None, ws: Optional[torch.Tensor] = None):
+    """(grad_q, grad_k, grad_v) from the forward call's inputs and results."""
     dev, T, B, Hq, H, D, ptrs = _prompt_args(q, k, v, offsets)
     s = _scale(scale, D)
     gs = _rows(grad_out, "grad_out", Hq, D, dev, T)
     _need(out, "out", torch.bfloat16, T * Hq * D, dev)
+    _need(out_rest, "out_rest", torch.bfloat16, T * Hq * D, dev)
     _need(lse, "lse", torch.float32, T * Hq, dev)
     gq = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
     gk = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
     gv = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
     with _on(dev) as stream:
         if ws is None:
-            need = int(L.lib().nf4_prompt_attention_bwd_workspace(T, Hq))
+            need = int(L.lib().nf4_prompt_attention_bwd_workspace(T, B, Hq, H, D))
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
         else:
             _need(ws, "ws", device=dev)
-        st = L.lib().nf4_prompt_attention_bwd(grad_out.data_ptr(), gs, *ptrs, out.data_ptr(), lse.data_ptr(), T,
-                                              offsets.data_ptr(), B, Hq, H, D, s, gq.data_ptr(), gk.data_ptr(),
-                                              gv.data_ptr(), 1, ws.data_ptr(), ws.numel() * ws.element_size(), stream)
+        st = L.lib().nf4_prompt_attention_bwd(grad_out.data_ptr(), gs, *ptrs, out.data_ptr(), _ptr(out_rest),
+                                              lse.data_ptr(), T, offsets.data_ptr(), B, Hq, H, D, s, gq.data_ptr(),
+                                              gk.data_ptr(), gv.data_ptr(), 1, ws.data_ptr(),
+                                              ws.numel() * ws.element_size(), stream)
     L.check("nf4_prompt_attention_bwd", st)
     return gq, gk, gv

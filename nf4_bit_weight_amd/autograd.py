@@ -104,15 +104,14 @@ def nf4_grouped_linear(x: torch.Tensor, offsets: torch.Tensor, w: NF4Weight, E: 
 
 class NF4PromptAttention(torch.autograd.Function):
     """Causal attention over packed sequences, differentiable in q, k and v.
-    Saved are the bf16 operands, the output and each row's log-sum-exp."""
+    Saved are the bf16 operands, the output with what its rounding took, and
+    each row's log-sum-exp."""
 
     @staticmethod
     def forward(ctx, q, k, v, offsets, scale):
         q2, k2, v2 = (_head_rows(t) for t in (q, k, v))
-        grad = any(ctx.needs_input_grad[:3])
-        out, lse = attention.nf4_prompt_attention_fwd(q2, k2, v2, offsets, scale, want_lse=grad)
-        if grad:
-            ctx.save_for_backward(q2, k2, v2, out, lse, offsets)
+        out, rest, lse = attention.nf4_prompt_attention_fwd(q2, k2, v2, offsets, scale, for_backward=True)
+        ctx.save_for_backward(q2, k2, v2, out, rest, lse, offsets)
         ctx.scale = scale
         ctx.dtypes = (q.dtype, k.dtype, v.dtype)
         return out.to(q.dtype)
@@ -120,8 +119,8 @@ class NF4PromptAttention(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_out):
-        q, k, v, out, lse, offsets = ctx.saved_tensors
-        grads = attention.nf4_prompt_attention_bwd(_head_rows(grad_out), q, k, v, out, lse, offsets, ctx.scale)
+        q, k, v, out, rest, lse, offsets = ctx.saved_tensors
+        grads = attention.nf4_prompt_attention_bwd(_head_rows(grad_out), q, k, v, out, rest, lse, offsets, ctx.scale)
         return (*(g.to(d) if need else None for g, d, need in zip(grads, ctx.dtypes, ctx.needs_input_grad)), None, None)
 
 
@@ -140,4 +139,7 @@ def nf4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offs
                          scale: float = None) -> torch.Tensor:
     """Causal attention inside each of the packed sequences that offsets
     (int32 [B + 1]) cut q [T, Hq, D] and k, v [T, Hkv, D] into; differentiable."""
-    return NF4PromptAttention.apply(q, k, v, offsets, scale)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        return NF4PromptAttention.apply(q, k, v, offsets, scale)
+    out = attention.nf4_prompt_attention_fwd(_head_rows(q), _head_rows(k), _head_rows(v), offsets, scale)
+    return out if out.dtype == q.dtype else out.to(q.dtype)

@@ -63,29 +63,30 @@ hipError_t launch_kv_attention(const KVAttnPlan& pl, const KVCache& c, const KVS
                                int64_t q_stride, int32_t Hq, float scale, void* out, int fill, void* ws,
                                hipStream_t stream);
 
-hipError_t launch_prompt_fwd(const PromptArgs& a, void* out, float* lse, hipStream_t stream);
+hipError_t launch_prompt_fwd(const PromptArgs& a, void* out, void* rest, float* lse, hipStream_t stream);
+size_t prompt_bwd_ws_bytes(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D);
 hipError_t launch_prompt_bwd(const PromptArgs& a, const void* grad_out, int64_t grad_stride, const void* out,
-                             const float* lse, void* grad_q, void* grad_k, void* grad_v, void* ws,
+                             const void* rest, const float* lse, void* grad_q, void* grad_k, void* grad_v, void* ws,
                              hipStream_t stream);
 
 // ---- device helpers ----------------------------------------------------------
 
-__device__ __forceinline__ int wave_sum(int x) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
-  return x;
+// Sum over the wave (the same in all lanes) and inclusive prefix sum, in the
+// vector unit's lane moves: rows of 16 lanes first, then across the rows.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int lane_move(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, false);
 }
-
-// Inclusive prefix sum over the wave.
 __device__ __forceinline__ int wave_scan(int x) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
+  x += lane_move<0x111, 0xF>(x);   // row_shr:1
+  x += lane_move<0x112, 0xF>(x);
+  x += lane_move<0x114, 0xF>(x);
+  x += lane_move<0x118, 0xF>(x);
+  x += lane_move<0x142, 0xA>(x);   // row_bcast:15 into rows 1 and 3
+  x += lane_move<0x143, 0xC>(x);   // row_bcast:31 into rows 2 and 3
   return x;
 }
+__device__ __forceinline__ int wave_sum(int x) { return __builtin_amdgcn_readlane(wave_scan(x), 63); }
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 

@@ -28,8 +28,9 @@ int check_heads(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
 int check_rows(const void* p, int64_t stride, int64_t T) {
   if (T == 0) return NF4_OK;
   if (!p) return NF4_ERR_NULL;
-  if (stride < 0 || stride > INT64_MAX / 4 / T) return NF4_ERR_SHAPE;
+  if (stride < 0) return NF4_ERR_SHAPE;
   if (stride % 8 || !aligned(p, 16)) return NF4_ERR_ALIGN;
+  if (stride > 1 << 24) return NF4_ERR_UNSUPPORTED;          // 64 rows lie within 32 bits of bytes
   return NF4_OK;
 }
 
@@ -145,7 +146,8 @@ int nf4_kv_attention(const void* q, int64_t q_stride, int64_t T, int32_t Hq, con
 
 int nf4_prompt_attention_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                              int64_t v_stride, int64_t T, const int32_t* offsets, int32_t B, int32_t Hq, int32_t Hkv,
-                             int32_t D, float scale, void* out, float* lse, int fill_outside, void* stream) {
+                             int32_t D, float scale, void* out, void* out_rest, float* lse, int fill_outside,
+                             void* stream) {
   int st = check_heads(T, B, Hq, Hkv, D);
   if (!st) st = check_rows(q, q_stride, T);
   if (!st) st = check_rows(k, k_stride, T);
@@ -153,25 +155,25 @@ int nf4_prompt_attention_fwd(const void* q, int64_t q_stride, const void* k, int
   if (st) return st;
   if (!(scale > 0.0f) || !std::isfinite(scale)) return NF4_ERR_SHAPE;
   if (!offsets || (T > 0 && !out)) return NF4_ERR_NULL;
-  if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(offsets, 4)) return NF4_ERR_ALIGN;
+  if (!aligned(out, 16) || !aligned(out_rest, 16) || !aligned(lse, 4) || !aligned(offsets, 4)) return NF4_ERR_ALIGN;
   if (T == 0) return NF4_OK;
   const PromptArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                      q_stride, k_stride, v_stride, offsets, static_cast<int32_t>(T), B, Hq, Hkv, D, scale,
                      fill_outside != 0};
-  const hipError_t e = launch_prompt_fwd(a, out, lse, static_cast<hipStream_t>(stream));
+  const hipError_t e = launch_prompt_fwd(a, out, out_rest, lse, static_cast<hipStream_t>(stream));
   if (e == hipSuccess) count_path(NF4_PATH_PROMPT_FWD);
   return to_status(e);
 }
 
-size_t nf4_prompt_attention_bwd_workspace(int64_t T, int32_t Hq) {
-  if (T < 0 || Hq < 1 || T > INT32_MAX / 4 || Hq > 1024) return SIZE_MAX;
-  return static_cast<size_t>(T) * Hq * sizeof(float);
+size_t nf4_prompt_attention_bwd_workspace(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
+  if (check_heads(T, B, Hq, Hkv, D)) return SIZE_MAX;
+  return T == 0 ? 0 : prompt_bwd_ws_bytes(T, B, Hq, Hkv, D);
 }
 
 int nf4_prompt_attention_bwd(const void* grad_out, int64_t grad_stride, const void* q, int64_t q_stride, const void* k,
-                             int64_t k_stride, const void* v, int64_t v_stride, const void* out, const float* lse,
-                             int64_t T, const int32_t* offsets, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
-                             float scale, void* grad_q, void* grad_k, void* grad_v, int fill_outside, void* ws,
+                             int64_t k_stride, const void* v, int64_t v_stride, const void* out, const void* out_rest,
+                             const float* lse, int64_t T, const int32_t* offsets, int32_t B, int32_t Hq, int32_t Hkv,
+                             int32_t D, float scale, void* grad_q, void* grad_k, void* grad_v, int fill_outside, void* ws,
                              size_t ws_bytes, void* stream) {
   int st = check_heads(T, B, Hq, Hkv, D);
   if (!st) st = check_rows(grad_out, grad_stride, T);
@@ -181,16 +183,16 @@ int nf4_prompt_attention_bwd(const void* grad_out, int64_t grad_stride, const vo
   if (st) return st;
   if (!(scale > 0.0f) || !std::isfinite(scale)) return NF4_ERR_SHAPE;
   if (!offsets || (T > 0 && (!out || !lse || !grad_q || !grad_k || !grad_v))) return NF4_ERR_NULL;
-  if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(grad_q, 16) || !aligned(grad_k, 16) || !aligned(grad_v, 16) ||
+  if (!aligned(out, 16) || !aligned(out_rest, 16) || !aligned(lse, 4) || !aligned(grad_q, 16) || !aligned(grad_k, 16) || !aligned(grad_v, 16) ||
       !aligned(offsets, 4))
     return NF4_ERR_ALIGN;
   if (T == 0) return NF4_OK;
-  if (!ws || ws_bytes < nf4_prompt_attention_bwd_workspace(T, Hq)) return NF4_ERR_WORKSPACE;
+  if (!ws || ws_bytes < prompt_bwd_ws_bytes(T, B, Hq, Hkv, D)) return NF4_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return NF4_ERR_ALIGN;
   const PromptArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                      q_stride, k_stride, v_stride, offsets, static_cast<int32_t>(T), B, Hq, Hkv, D, scale,
                      fill_outside != 0};
-  const hipError_t e = launch_prompt_bwd(a, grad_out, grad_stride, out, lse, grad_q, grad_k, grad_v, ws,
+  const hipError_t e = launch_prompt_bwd(a, grad_out, grad_stride, out, out_rest, lse, grad_q, grad_k, grad_v, ws,
                                          static_cast<hipStream_t>(stream));
   if (e == hipSuccess) count_path(NF4_PATH_PROMPT_BWD);
   return to_status(e);

@@ -8,7 +8,10 @@
 // layout: the contraction runs over the streamed rows in the order the first
 // product left them (8 j + 4 (lane >> 5) + i), and the streamed tile is read
 // transposed in that same order.
+#include <type_traits>
+
 #include "nf4_attn.hpp"
+#include "nf4_internal.hpp"
 
 namespace nf4 {
 
@@ -23,10 +26,10 @@ constexpr int kRows = 128;      // register rows per workgroup (32 a wave)
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 // Copies straight into LDS, invisible to the compiler's own waits; the kernel
-// waits for them itself (vm_wait).  The LDS address is uniform, lane i lands
+// waits for them itself (land).  The LDS address is uniform, lane i lands
 // 16 i (4 i) bytes behind it.
-__device__ __forceinline__ void dma_b128(const void* src, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(src), "{m0}"(lds) : "memory");
+__device__ __forceinline__ void dma_b128(uint32_t off, const char* base, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" :: "v"(off), "s"(base), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void dma_b32(const void* src, uint32_t lds) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" :: "v"(src), "{m0}"(lds) : "memory");
@@ -34,57 +37,73 @@ __device__ __forceinline__ void dma_b32(const void* src, uint32_t lds) {
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_void_t*)p));
 }
-__device__ __forceinline__ void land() {                       // every copy has landed, for every wave
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+// All but this wave's last N copies have landed, and every wave is here.
+template <int N = 0>
+__device__ __forceinline__ void land() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"(N) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
-// LDS tile [64][D]: the 16-byte chunk c of row r lies at chunk c ^ turn(r).  Both
-// reads are free of bank conflicts: 16 bytes of 8 neighbouring rows, and the
-// transposed read's 32 bytes of 8 rows.
-template <int D>
-__device__ __forceinline__ int turn(int r) {
-  return D == 128 ? 2 * (r & 7) + ((r >> 3) & 1) : 2 * ((r >> 1) & 3) + ((r >> 3) & 1);
-}
-
-// Copies rows row0 .. row0+63 of a sequence of n rows (the last row again
-// behind the end; its scores are masked) into an LDS tile.
-template <int D>
-__device__ __forceinline__ void copy_tile(const uint16_t* base, int64_t stride, int row0, int n, const void* tile) {
-  constexpr int C = D / 8, N = kTile * C / 256;
-  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int k = (i * 4 + wave) * 64 + lane, r = k / C, c = (k % C) ^ turn<D>(r);
-    dma_b128(base + min(row0 + r, n - 1) * stride + 8 * c, lds_addr(tile) + (i * 4 + wave) * 1024);
+// LDS tile of TR rows (64 or 32): [D / 32 slices of 32 elements][TR rows][64
+// bytes], the 16-byte chunk c of a row's slice at chunk c ^ ((row >> 2) & 3).
+// Both reads are free of bank conflicts (16 bytes of 8 neighbouring rows; the
+// transposed read's 32 bytes of 8 rows), and slice and row are immediate offsets
+// from two lane addresses each.
+//
+// Copier copies rows row0 .. row0+TR-1 of a sequence of n rows (the last row
+// again behind the end; its scores are masked) into such a tile: 16 rows of
+// one slice an instruction, kCopies instructions a wave.
+template <int D, int TR>
+struct Copier {
+  static constexpr int kCopies = D / 32 * TR / 64;
+  uint32_t off, stride;                                         // bytes
+  int row;
+  __device__ __forceinline__ explicit Copier(int64_t stride_elems) {
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    row = 16 * (TR == 64 ? wave : wave & 1) + (lane >> 2);
+    stride = static_cast<uint32_t>(stride_elems) * 2;
+    off = 16 * ((lane & 3) ^ ((row >> 2) & 3));
   }
-}
-
-// Lane offsets (bytes) of the two kinds of reads.
-template <int D>
-struct Offs {
-  int row[D / 16];          // chunk 2 ks + h of row (lane & 31)
-  int tr[D / 32][2];        // transposed: rows 4h + i (+ 8), elements 32 dt + ..
-  __device__ __forceinline__ Offs() {
-    const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  __device__ __forceinline__ void operator()(const uint16_t* seq, int row0, int n, const void* tile) const {
+    const int wave = uniform(threadIdx.x >> 6), first = TR == 64 ? 0 : wave >> 1;
+    const char* base = reinterpret_cast<const char*>(seq) + static_cast<int64_t>(row0) * stride + 64 * first;
+    const uint32_t lds = lds_addr(tile) + 1024 * (TR == 64 ? wave : wave & 1) + TR * 64 * first;
+    const uint32_t o = static_cast<uint32_t>(min(row, n - 1 - row0)) * stride + off;
+    constexpr int kStep = TR == 64 ? 1 : 2;
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) row[ks] = l32 * D * 2 + (((2 * ks + h) ^ turn<D>(l32)) << 4);
-#pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt)
-#pragma unroll
-      for (int hi = 0; hi < 2; ++hi) {
-        const int r = 4 * h + ((lane & 15) >> 2) + 8 * hi;
-        const int col = 32 * dt + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-        tr[dt][hi] = r * D * 2 + (((col >> 3) ^ turn<D>(r)) << 4) + (col & 7) * 2;
-      }
+    for (int i = 0; i < kCopies; ++i) dma_b128(o, base + 64 * kStep * i, lds + TR * 64 * kStep * i);
   }
 };
 
-__device__ __forceinline__ bf16x8_t read_row(const char* p) { return *reinterpret_cast<const bf16x8_t*>(p); }
-__device__ __forceinline__ bf16x8_t read_tr(const char* lo, const char* hi) {
-  const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)lo);
-  const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)hi);
+// Lane addresses (bytes) of the two kinds of reads.
+struct Offs {
+  int row[2];               // row (lane & 31), chunks 2 ks + h of even and odd ks
+  int tr[2];                // transposed: rows 4h + i (+ 8)
+  __device__ __forceinline__ Offs() {
+    const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) row[p] = l32 * 64 + (((2 * p + h) ^ ((l32 >> 2) & 3)) << 4);
+#pragma unroll
+    for (int hi = 0; hi < 2; ++hi) {
+      const int r = 4 * h + ((lane & 15) >> 2) + 8 * hi;
+      const int col = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+      tr[hi] = r * 64 + (((col >> 3) ^ ((r >> 2) & 3)) << 4) + (col & 7) * 2;
+    }
+  }
+};
+
+// elements 16 ks + 8 h .. +7 of row 32 w + (lane & 31)
+template <int TR>
+__device__ __forceinline__ bf16x8_t read_row(const char* tile, const Offs& o, int w, int ks) {
+  return *reinterpret_cast<const bf16x8_t*>(tile + (ks >> 1) * (TR * 64) + w * 2048 + o.row[ks & 1]);
+}
+// element 32 dt + (lane & 31) of rows 16 m + 4 h .. +3 and 16 m + 8 + 4 h .. +3
+template <int TR>
+__device__ __forceinline__ bf16x8_t read_tr(const char* tile, const Offs& o, int m, int dt) {
+  const char* p = tile + dt * (TR * 64) + m * 1024;
+  const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + o.tr[0]));
+  const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + o.tr[1]));
   const u32x2_t x = __builtin_bit_cast(u32x2_t, a), y = __builtin_bit_cast(u32x2_t, b);
   return __builtin_bit_cast(bf16x8_t, u32x4_t{x[0], x[1], y[0], y[1]});
 }
@@ -106,35 +125,63 @@ __device__ __forceinline__ bf16x8_t pack8(const f32x16_t& p, int m) {
                                               pack_bf16x2(p[8 * m + 4], p[8 * m + 5]), pack_bf16x2(p[8 * m + 6], p[8 * m + 7])});
 }
 
-// The z-th tile of `rows` rows, counted over all sequences; false behind the last.
+// The tiles of 128 rows of all sequences, heaviest first: a sequence of t tiles
+// has one tile of each weight t, t-1, .. 1 (tiles of other rows that it works
+// through).  The z-th is found by bisection over the weight w, with
+// C(w) = sum_b max(0, t_b - w + 1) tiles of weight w or more.  False behind the
+// last tile.
 struct TileAt {
-  int first, n, tile;
+  int first, n, weight;
 };
-__device__ __forceinline__ int count_tiles(const PromptArgs& a, int rows) {
-  int sum = 0;
-  for (int b = threadIdx.x & 63; b < a.B; b += 64) {
-    int f, n;
-    seq_rows(a.offsets, b, a.T, f, n);
-    sum += (n + rows - 1) / rows;
-  }
-  return uniform(wave_sum(sum));
-}
-__device__ __forceinline__ bool find_tile(const PromptArgs& a, int rows, int z, TileAt& at) {
-  int base = 0;
+__device__ __forceinline__ bool find_tile(const PromptArgs& a, int z, TileAt& at) {
   const int lane = threadIdx.x & 63;
+  auto tiles_of = [&](int b, int& f, int& n) __attribute__((always_inline)) {
+    f = n = 0;
+    if (b < a.B) seq_rows(a.offsets, b, a.T, f, n);
+    return (n + kRows - 1) / kRows;
+  };
+  int f0, n0;
+  const int t0 = tiles_of(lane, f0, n0);                        // the first 64 sequences stay in registers
+  auto at_least = [&](int w) __attribute__((always_inline)) {
+    int c = max(0, t0 - w + 1);
+    for (int b = lane + 64; b < a.B; b += 64) {
+      int f, n;
+      c += max(0, tiles_of(b, f, n) - w + 1);
+    }
+    return uniform(wave_sum(c));
+  };
+  int lo = 1, hi = (a.T + kRows - 1) / kRows, above = 0;        // C(lo) > z once found, C(hi + 1) = above <= z
+  if (a.B == 1) {
+    lo = uniform(__shfl(t0, 0)) - z;
+    if (lo < 1) return false;
+    above = z;
+  } else {
+    if (at_least(1) <= z) return false;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2, c = at_least(mid);
+      if (c > z) {
+        lo = mid;
+      } else {
+        hi = mid - 1;
+        above = c;
+      }
+    }
+  }
+  int k = z - above;                                            // the k-th sequence with that many tiles
   for (int b0 = 0; b0 < a.B; b0 += 64) {
-    int f = 0, n = 0;
-    if (b0 + lane < a.B) seq_rows(a.offsets, b0 + lane, a.T, f, n);
-    const int tiles = (n + rows - 1) / rows, incl = wave_scan(tiles);
-    const uint64_t hit = __ballot(base + incl > z);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
+    int f = f0, n = n0;
+    const int t = b0 == 0 ? t0 : tiles_of(b0 + lane, f, n);
+    uint64_t has = __ballot(t >= lo);
+    const int c = __popcll(has);
+    if (k < c) {
+      for (; k > 0; --k) has &= has - 1;
+      const int l = __builtin_ctzll(has);
       at.first = uniform(__shfl(f, l));
       at.n = uniform(__shfl(n, l));
-      at.tile = uniform(z - base - __shfl(incl - tiles, l));
+      at.weight = lo;
       return true;
     }
-    base += __shfl(incl, 63);
+    k -= c;
   }
   return false;
 }
@@ -155,28 +202,33 @@ __device__ __forceinline__ void fill_rows(const PromptArgs& a, uint16_t* out, in
 __device__ __forceinline__ int head_of(int x, int heads) { return heads % 8 == 0 ? (x % 8) * (heads / 8) + x / 8 : x; }
 
 // ---- forward -------------------------------------------------------------------
+// One workgroup: 128 query rows of one head, streaming keys and values.  The
+// running maximum moves only when a score passes it by 2^kSlack, so the
+// rescaling of the sums is rare; weights are then at most 2^kSlack, which
+// costs bf16 and fp32 nothing.
+constexpr float kSlack = 8.0f;
+
 template <int D>
-__global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* __restrict__ out, float* __restrict__ lse,
-                                                       int bound) {
+__global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* __restrict__ out,
+                                                       uint16_t* __restrict__ rest, float* __restrict__ lse, int bound) {
   constexpr int KS = D / 16, DT = D / 32;
   __shared__ __align__(1024) char lds[2][2][kTile * D * 2];     // [buffer][keys, values]
   const int x = blockIdx.x % a.Hq, z = blockIdx.x / a.Hq;
   const int hq = head_of(x, a.Hq), hk = hq / (a.Hq / a.Hkv);
   fill_rows(a, out, a.Hq, hq, z, bound);
-  const int total = count_tiles(a, kRows);
+  if (rest) fill_rows(a, rest, a.Hq, hq, z, bound);
   TileAt at;
-  // long rows of keys first
-  if (z >= total || !find_tile(a, kRows, total - 1 - z, at)) return;
+  if (!find_tile(a, z, at)) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), l32 = lane & 31, h = lane >> 5;
-  const int w0 = at.tile * kRows + 32 * wave, qi = w0 + l32;
+  const int q0 = (at.weight - 1) * kRows, w0 = q0 + 32 * wave, qi = w0 + l32;
   const float c = a.scale * kLog2e;
-  const Offs<D> of;
-
+  const Offs of;
+  const Copier<D, 64> ck(a.k_stride), cv(a.v_stride);
   const uint16_t* kb = a.k + at.first * a.k_stride + hk * D;
   const uint16_t* vb = a.v + at.first * a.v_stride + hk * D;
-  copy_tile<D>(kb, a.k_stride, 0, at.n, lds[0][0]);
-  copy_tile<D>(vb, a.v_stride, 0, at.n, lds[0][1]);
-
+  const int tiles = (min(at.n, q0 + kRows) + kTile - 1) / kTile;
+  const int whole = q0 / kTile;                                 // tiles that every row sees whole: an even number
+  ck(kb, 0, at.n, lds[0][0]);
   bf16x8_t qf[KS];
   {
     const uint16_t* src = a.q + (static_cast<int64_t>(at.first) + min(qi, at.n - 1)) * a.q_stride + hq * D + 8 * h;
@@ -186,177 +238,221 @@ __global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* _
   f32x16_t acc[DT];
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt) acc[dt] = zero16();
-  float mx = -INFINITY, sum = 0.0f;
+  float ref = -INFINITY, sum[2] = {0.0f, 0.0f};                 // ref: the maximum in use, times c
 
-  const int tiles = (min(at.n, at.tile * kRows + kRows) + kTile - 1) / kTile;
-  for (int j = 0; j < tiles; ++j) {
-    land();
-    if (j + 1 < tiles) {
-      copy_tile<D>(kb, a.k_stride, (j + 1) * kTile, at.n, lds[(j + 1) & 1][0]);
-      copy_tile<D>(vb, a.v_stride, (j + 1) * kTile, at.n, lds[(j + 1) & 1][1]);
-    }
-    if (j * kTile > w0 + 31) continue;                          // behind every row of this wave
+  auto scores = [&](int j, f32x16_t (&s)[2]) __attribute__((always_inline)) {
     const char* kt = lds[j & 1][0];
-    const char* vt = lds[j & 1][1];
-    f32x16_t s[2] = {zero16(), zero16()};
+    s[0] = zero16();
+    s[1] = zero16();
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int w = 0; w < 2; ++w) s[w] = mfma(read_row(kt + of.row[ks] + 32 * w * D * 2), qf[ks], s[w]);
-    if (j * kTile + kTile - 1 > w0) {
+      for (int w = 0; w < 2; ++w) s[w] = mfma(read_row<64>(kt, of, w, ks), qf[ks], s[w]);
+  };
+  auto maximum = [&](const f32x16_t (&s)[2]) __attribute__((always_inline)) {
+    float top = s[0][0];
 #pragma unroll
-      for (int w = 0; w < 2; ++w)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (j * kTile + 32 * w + reg_row(r) + 4 * h > qi) s[w][r] = -INFINITY;
-    }
-    float top = mx;
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[w][r]);
-    top = half_max(top);
-    const float ref = top == -INFINITY ? 0.0f : top * c;
-    if (__any(top != mx)) {
-      const float f = __builtin_amdgcn_exp2f(__builtin_fmaf(mx, c, -ref));
-      sum *= f;
+    for (int r = 1; r < 31; r += 2) top = fmaxf(fmaxf(top, s[r / 16][r % 16]), s[(r + 1) / 16][(r + 1) % 16]);
+    top = half_max(fmaxf(top, s[1][15])) * c;
+    if (__any(top > ref + kSlack)) {
+      const float to = fmaxf(top, ref), f = to == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ref - to);
+      sum[0] *= f;
+      sum[1] *= f;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[dt][r] *= f;
-      mx = top;
+      ref = to;
     }
+  };
+  auto weigh = [&](int j, f32x16_t (&s)[2]) __attribute__((always_inline)) {
+    const char* vt = lds[j & 1][1];
+    const float m = ref == -INFINITY ? 0.0f : ref;
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+    for (int w = 0; w < 2; ++w) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        s[w][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[w][r], c, -ref));
-        sum += s[w][r];
+        s[w][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[w][r], c, -m));
+        sum[w] += s[w][r];
       }
+#pragma unroll
+      for (int mm = 0; mm < 2; ++mm) {
+        const bf16x8_t pf = pack8(s[w], mm);
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) acc[dt] = mfma(read_tr<64>(vt, of, 2 * w + mm, dt), pf, acc[dt]);
+      }
+    }
+  };
+
+  // The scores of tile j+1 are formed while the weights of tile j are computed:
+  // the two are independent, so matrix and vector instructions of one wave
+  // overlap.  Keys therefore run one tile ahead of values.
+  auto advance = [&](int j) __attribute__((always_inline)) {
+    land();
+    if (j + 2 < tiles) ck(kb, (j + 2) * kTile, at.n, lds[j & 1][0]);
+    if (j + 1 < tiles) cv(vb, (j + 1) * kTile, at.n, lds[(j + 1) & 1][1]);
+  };
+  f32x16_t s0[2], s1[2];
+  land();
+  if (1 < tiles) ck(kb, kTile, at.n, lds[1][0]);
+  cv(vb, 0, at.n, lds[0][1]);
+  scores(0, s0);
+  for (int j = 0; j < whole; j += 2) {
+    advance(j);
+    maximum(s0);
+    scores(j + 1, s1);
+    weigh(j, s0);
+    advance(j + 1);
+    maximum(s1);
+    scores(j + 2, s0);
+    weigh(j + 1, s1);
+  }
+  for (int j = whole; j < tiles; ++j) {                         // at most two, on the diagonal
+    advance(j);
+    if (j * kTile > w0 + 31) continue;                          // behind every row of this wave
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const bf16x8_t pf = pack8(s[w], m);
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-          const char* p = vt + (32 * w + 16 * m) * D * 2;
-          acc[dt] = mfma(read_tr(p + of.tr[dt][0], p + of.tr[dt][1]), pf, acc[dt]);
-        }
-      }
+      for (int r = 0; r < 16; ++r)
+        if (j * kTile + 32 * w + reg_row(r) + 4 * h > qi) s0[w][r] = -INFINITY;
+    maximum(s0);
+    weigh(j, s0);
+    if (j + 1 < tiles) scores(j + 1, s0);
   }
-  sum = half_sum(sum);
+  const float total = half_sum(sum[0] + sum[1]);
   if (qi >= at.n) return;
-  const float f = 1.0f / sum;                                   // every row sees itself
+  const float f = 1.0f / total;                                 // every row sees itself
   const int64_t t = static_cast<int64_t>(at.first) + qi;
-  if (lse && h == 0) lse[static_cast<int64_t>(hq) * a.T + t] = (__builtin_amdgcn_logf(sum) + mx * c) * kLn2;
-  uint16_t* dst = out + (t * a.Hq + hq) * D + 4 * h;
+  if (lse && h == 0) lse[static_cast<int64_t>(hq) * a.T + t] = (__builtin_amdgcn_logf(total) + ref) * kLn2;
+  const int64_t dst = (t * a.Hq + hq) * D + 4 * h;
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-      *reinterpret_cast<uint2*>(dst + 32 * dt + 8 * b) =
-          make_uint2(pack_bf16x2(acc[dt][4 * b] * f, acc[dt][4 * b + 1] * f),
-                     pack_bf16x2(acc[dt][4 * b + 2] * f, acc[dt][4 * b + 3] * f));
+    for (int b = 0; b < 4; ++b) {
+      const float y[4] = {acc[dt][4 * b] * f, acc[dt][4 * b + 1] * f, acc[dt][4 * b + 2] * f, acc[dt][4 * b + 3] * f};
+      const uint2 o = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+      *reinterpret_cast<uint2*>(out + dst + 32 * dt + 8 * b) = o;
+      // what the rounding took, for the backward pass
+      if (rest)
+        *reinterpret_cast<uint2*>(rest + dst + 32 * dt + 8 * b) =
+            make_uint2(pack_bf16x2(y[0] - __builtin_bit_cast(float, o.x << 16), y[1] - __builtin_bit_cast(float, o.x & 0xFFFF0000u)),
+                       pack_bf16x2(y[2] - __builtin_bit_cast(float, o.y << 16), y[3] - __builtin_bit_cast(float, o.y & 0xFFFF0000u)));
+    }
 }
 
 // ---- backward --------------------------------------------------------------------
-// delta[hq][t] = grad_out[t, hq] . out[t, hq], in fp32: D / 8 lanes a row.
-template <int D>
-__global__ __launch_bounds__(256) void k_prompt_delta(PromptArgs a, const uint16_t* __restrict__ go, int64_t go_stride,
-                                                      const uint16_t* __restrict__ out, float* __restrict__ delta) {
-  constexpr int L = D / 8;
-  const int64_t rows = static_cast<int64_t>(a.T) * a.Hq;
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / L; i < rows;
-       i += static_cast<int64_t>(gridDim.x) * 256 / L) {
-    const int64_t t = i / a.Hq;
-    const int hq = static_cast<int>(i - t * a.Hq), e = 8 * (threadIdx.x % L);
-    const u32x4_t x = *reinterpret_cast<const u32x4_t*>(go + t * go_stride + hq * D + e);
-    const u32x4_t y = *reinterpret_cast<const u32x4_t*>(out + i * D + e);
-    float s = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      s = __builtin_fmaf(__builtin_bit_cast(float, x[k] << 16), __builtin_bit_cast(float, y[k] << 16), s);
-      s = __builtin_fmaf(__builtin_bit_cast(float, x[k] & 0xFFFF0000u), __builtin_bit_cast(float, y[k] & 0xFFFF0000u), s);
-    }
-#pragma unroll
-    for (int d = 1; d < L; d *= 2) s += __shfl_xor(s, d);
-    if (e == 0) delta[static_cast<int64_t>(hq) * a.T + t] = s;
-  }
-}
+struct GradArgs {
+  const uint16_t *go, *out, *rest;
+  int64_t go_stride;
+  const float* lse;
+  float* stat;              // [2][Hq][T]: lse log2(e) and delta, grad_q's kernel to grad_k's
+};
 
 // grad_q: a wave keeps 32 query rows and streams keys and values.
-//   P = exp(scale S - lse), dS = P (dP - delta), grad_q = scale dS K
+//   delta = dO . O, P = exp(scale S - lse), dS = P (dO V^T - delta), grad_q = scale dS K
 template <int D>
-__global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, const uint16_t* __restrict__ go, int64_t go_stride,
-                                                         const float* __restrict__ lse, const float* __restrict__ delta,
-                                                         uint16_t* __restrict__ gq, int bound) {
+__global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, GradArgs g, uint16_t* __restrict__ gq, int bound) {
   constexpr int KS = D / 16, DT = D / 32;
   __shared__ __align__(1024) char lds[2][2][kTile * D * 2];
   const int x = blockIdx.x % a.Hq, z = blockIdx.x / a.Hq;
   const int hq = head_of(x, a.Hq), hk = hq / (a.Hq / a.Hkv);
   fill_rows(a, gq, a.Hq, hq, z, bound);
-  const int total = count_tiles(a, kRows);
   TileAt at;
-  if (z >= total || !find_tile(a, kRows, total - 1 - z, at)) return;
+  if (!find_tile(a, z, at)) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), l32 = lane & 31, h = lane >> 5;
-  const int w0 = at.tile * kRows + 32 * wave, qi = w0 + l32;
+  const int q0 = (at.weight - 1) * kRows, w0 = q0 + 32 * wave, qi = w0 + l32;
   const float c = a.scale * kLog2e;
-  const Offs<D> of;
+  const Offs of;
+  const Copier<D, 64> ck(a.k_stride), cv(a.v_stride);
   const uint16_t* kb = a.k + at.first * a.k_stride + hk * D;
   const uint16_t* vb = a.v + at.first * a.v_stride + hk * D;
-  copy_tile<D>(kb, a.k_stride, 0, at.n, lds[0][0]);
-  copy_tile<D>(vb, a.v_stride, 0, at.n, lds[0][1]);
+  const int tiles = (min(at.n, q0 + kRows) + kTile - 1) / kTile;
+  const int whole = q0 / kTile;                                 // tiles that every row sees whole
+  ck(kb, 0, at.n, lds[0][0]);
+  cv(vb, 0, at.n, lds[0][1]);
 
   const int64_t t = static_cast<int64_t>(at.first) + min(qi, at.n - 1);
   bf16x8_t qf[KS], gf[KS];
+  float delta = 0.0f;
+  {
+    const uint16_t* qs = a.q + t * a.q_stride + hq * D + 8 * h;
+    const uint16_t* gs = g.go + t * g.go_stride + hq * D + 8 * h;
+    const int64_t os = (t * a.Hq + hq) * D + 8 * h;
 #pragma unroll
-  for (int ks = 0; ks < KS; ++ks) {
-    qf[ks] = *reinterpret_cast<const bf16x8_t*>(a.q + t * a.q_stride + hq * D + 8 * h + 16 * ks);
-    gf[ks] = *reinterpret_cast<const bf16x8_t*>(go + t * go_stride + hq * D + 8 * h + 16 * ks);
+    for (int ks = 0; ks < KS; ++ks) {
+      qf[ks] = *reinterpret_cast<const bf16x8_t*>(qs + 16 * ks);
+      gf[ks] = *reinterpret_cast<const bf16x8_t*>(gs + 16 * ks);
+    }
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const bf16x8_t o = *reinterpret_cast<const bf16x8_t*>(g.out + os + 16 * ks);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) delta = __builtin_fmaf(static_cast<float>(gf[ks][i]), static_cast<float>(o[i]), delta);
+    }
+    if (g.rest) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const bf16x8_t o = *reinterpret_cast<const bf16x8_t*>(g.rest + os + 16 * ks);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) delta = __builtin_fmaf(static_cast<float>(gf[ks][i]), static_cast<float>(o[i]), delta);
+      }
+    }
   }
-  const float ls = lse[static_cast<int64_t>(hq) * a.T + t] * kLog2e, dl = delta[static_cast<int64_t>(hq) * a.T + t];
+  delta = half_sum(delta);
+  const int64_t st = static_cast<int64_t>(hq) * a.T + t;
+  const float ls = g.lse[st] * kLog2e;
+  if (qi < at.n && h == 0) {
+    g.stat[st] = ls;
+    g.stat[static_cast<int64_t>(a.Hq) * a.T + st] = delta;
+  }
   f32x16_t acc[DT];
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt) acc[dt] = zero16();
 
-  const int tiles = (min(at.n, at.tile * kRows + kRows) + kTile - 1) / kTile;
-  for (int j = 0; j < tiles; ++j) {
+  struct Pair {
+    f32x16_t s, dp;
+  };
+  auto scores = [&](int j, int w, Pair& p) __attribute__((always_inline)) {
+    const char* kt = lds[j & 1][0];
+    const char* vt = lds[j & 1][1];
+    p.s = zero16();
+    p.dp = zero16();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      p.s = mfma(read_row<64>(kt, of, w, ks), qf[ks], p.s);
+      p.dp = mfma(read_row<64>(vt, of, w, ks), gf[ks], p.dp);
+    }
+  };
+  auto apply = [&](int j, int w, Pair& p, auto masked) __attribute__((always_inline)) {
+    const char* kt = lds[j & 1][0];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      p.s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(p.s[r], c, -ls)) * (p.dp[r] - delta);
+      if constexpr (decltype(masked)::value)
+        if (j * kTile + 32 * w + reg_row(r) + 4 * h > qi) p.s[r] = 0.0f;
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const bf16x8_t pf = pack8(p.s, m);
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) acc[dt] = mfma(read_tr<64>(kt, of, 2 * w + m, dt), pf, acc[dt]);
+    }
+  };
+  auto step = [&](int j, auto masked) __attribute__((always_inline)) {
     land();
     if (j + 1 < tiles) {
-      copy_tile<D>(kb, a.k_stride, (j + 1) * kTile, at.n, lds[(j + 1) & 1][0]);
-      copy_tile<D>(vb, a.v_stride, (j + 1) * kTile, at.n, lds[(j + 1) & 1][1]);
+      ck(kb, (j + 1) * kTile, at.n, lds[(j + 1) & 1][0]);
+      cv(vb, (j + 1) * kTile, at.n, lds[(j + 1) & 1][1]);
     }
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int k0 = j * kTile + 32 * w;
-      if (k0 > w0 + 31) continue;
-      const char* kt = lds[j & 1][0] + 32 * w * D * 2;
-      const char* vt = lds[j & 1][1] + 32 * w * D * 2;
-      f32x16_t s = zero16(), dp = zero16();
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        s = mfma(read_row(kt + of.row[ks]), qf[ks], s);
-        dp = mfma(read_row(vt + of.row[ks]), gf[ks], dp);
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, -ls)) * (dp[r] - dl);
-      if (k0 + 31 > w0) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (k0 + reg_row(r) + 4 * h > qi) s[r] = 0.0f;
-      }
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const bf16x8_t pf = pack8(s, m);
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-          const char* p = kt + 16 * m * D * 2;
-          acc[dt] = mfma(read_tr(p + of.tr[dt][0], p + of.tr[dt][1]), pf, acc[dt]);
-        }
-      }
-    }
-  }
+    if (decltype(masked)::value && j * kTile > w0 + 31) return;  // behind every row of this wave
+    Pair p0, p1;
+    scores(j, 0, p0);
+    scores(j, 1, p1);
+    apply(j, 0, p0, masked);
+    apply(j, 1, p1, masked);
+  };
+  for (int j = 0; j < whole; ++j) step(j, std::false_type{});
+  for (int j = whole; j < tiles; ++j) step(j, std::true_type{});  // at most two, on the diagonal
   if (qi >= at.n) return;
   uint16_t* dst = gq + (t * a.Hq + hq) * D + 4 * h;
 #pragma unroll
@@ -371,35 +467,42 @@ __global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, const uin
 // grad_k and grad_v: a wave keeps 32 keys with their values and streams the
 // queries and output gradients of every query head of the group, in order.
 //   grad_v = P^T dO, grad_k = scale dS^T Q
+// Where the tiles alone leave compute units idle, the heads of a group are
+// split over `parts` workgroups, whose fp32 sums k_prompt_join adds in order.
 template <int D>
-__global__ __launch_bounds__(256, 1) void k_prompt_bwd_kv(PromptArgs a, const uint16_t* __restrict__ go, int64_t go_stride,
-                                                          const float* __restrict__ lse, const float* __restrict__ delta,
-                                                          uint16_t* __restrict__ gk, uint16_t* __restrict__ gv, int bound) {
+__global__ __launch_bounds__(256, 1) void k_prompt_bwd_kv(PromptArgs a, GradArgs g, uint16_t* __restrict__ gk,
+                                                          uint16_t* __restrict__ gv, float* __restrict__ part, int parts,
+                                                          int bound) {
   constexpr int KS = D / 16, DT = D / 32;
   __shared__ __align__(1024) char lds[2][2][kTile * D * 2];     // [buffer][queries, output gradients]
   __shared__ __align__(256) float stat[2][2][kTile];            // [buffer][lse, delta]
-  const int x = blockIdx.x % a.Hkv, z = blockIdx.x / a.Hkv, G = a.Hq / a.Hkv;
-  const int hk = head_of(x, a.Hkv);
-  fill_rows(a, gk, a.Hkv, hk, z, bound);
-  fill_rows(a, gv, a.Hkv, hk, z, bound);
+  const int x = blockIdx.x % (a.Hkv * parts), z = blockIdx.x / (a.Hkv * parts);
+  const int hk = head_of(x / parts, a.Hkv), pt = x % parts;
+  const int g0 = a.Hq / a.Hkv * pt / parts, G = a.Hq / a.Hkv * (pt + 1) / parts - g0;   // heads g0 .. g0+G-1 of the group
+  const int h0 = hk * (a.Hq / a.Hkv) + g0;
+  if (pt == 0) {
+    fill_rows(a, gk, a.Hkv, hk, z, bound);
+    fill_rows(a, gv, a.Hkv, hk, z, bound);
+  }
   TileAt at;
-  if (!find_tile(a, kRows, z, at)) return;
+  if (!find_tile(a, z, at)) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), l32 = lane & 31, h = lane >> 5;
-  const int w0 = at.tile * kRows + 32 * wave, ki = w0 + l32;
+  const int k0 = ((at.n + kRows - 1) / kRows - at.weight) * kRows, w0 = k0 + 32 * wave, ki = w0 + l32;
   const float c = a.scale * kLog2e;
-  const Offs<D> of;
-  const int q0 = at.tile * kRows / kTile;                       // first query tile that sees these keys
-  const int per = (at.n + kTile - 1) / kTile - q0, steps = per * G;
-  auto copy_step = [&](int st) __attribute__((always_inline)) {
-    const int hq = hk * G + st / per, j = q0 + st % per, buf = st & 1;
-    copy_tile<D>(a.q + at.first * a.q_stride + hq * D, a.q_stride, j * kTile, at.n, lds[buf][0]);
-    copy_tile<D>(go + at.first * go_stride + hq * D, go_stride, j * kTile, at.n, lds[buf][1]);
+  const Offs of;
+  const Copier<D, 64> cq(a.q_stride), cg(g.go_stride);
+  const int j0 = k0 / kTile;                                    // first query tile that sees these keys
+  const int per = (at.n + kTile - 1) / kTile - j0;
+  const uint16_t* qb = a.q + at.first * a.q_stride + h0 * D;
+  const uint16_t* gb = g.go + at.first * g.go_stride + h0 * D;
+  auto copy_step = [&](int buf, int i, int j) __attribute__((always_inline)) {
+    cq(qb + i * D, j * kTile, at.n, lds[buf][0]);
+    cg(gb + i * D, j * kTile, at.n, lds[buf][1]);
     if (wave < 2) {
-      const int64_t row = static_cast<int64_t>(hq) * a.T + at.first + min(j * kTile + lane, at.n - 1);
-      dma_b32((wave == 0 ? lse : delta) + row, lds_addr(stat[buf][wave]));
+      const int64_t row = (static_cast<int64_t>(wave) * a.Hq + h0 + i) * a.T + at.first + min(j * kTile + lane, at.n - 1);
+      dma_b32(g.stat + row, lds_addr(stat[buf][wave]));
     }
   };
-  copy_step(0);
 
   const int64_t t = static_cast<int64_t>(at.first) + min(ki, at.n - 1);
   bf16x8_t kf[KS], vf[KS];
@@ -415,57 +518,98 @@ __global__ __launch_bounds__(256, 1) void k_prompt_bwd_kv(PromptArgs a, const ui
     av[dt] = zero16();
   }
 
-  for (int st = 0; st < steps; ++st) {
-    land();
-    if (st + 1 < steps) copy_step(st + 1);
-    const int j = q0 + st % per;
+  struct Pair {
+    f32x16_t s, dp;
+  };
+  auto scores = [&](int buf, int w, Pair& p) __attribute__((always_inline)) {
+    const char* qt = lds[buf][0];
+    const char* gt = lds[buf][1];
+    p.s = zero16();
+    p.dp = zero16();
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int r0 = j * kTile + 32 * w;
-      if (r0 + 31 < w0) continue;                               // before every key of this wave
-      const char* qt = lds[st & 1][0] + 32 * w * D * 2;
-      const char* gt = lds[st & 1][1] + 32 * w * D * 2;
-      f32x16_t s = zero16(), dp = zero16();
+    for (int ks = 0; ks < KS; ++ks) {
+      p.s = mfma(read_row<64>(qt, of, w, ks), kf[ks], p.s);
+      p.dp = mfma(read_row<64>(gt, of, w, ks), vf[ks], p.dp);
+    }
+  };
+  auto weigh = [&](int buf, int j, int w, Pair& p, auto masked) __attribute__((always_inline)) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        s = mfma(read_row(qt + of.row[ks]), kf[ks], s);
-        dp = mfma(read_row(gt + of.row[ks]), vf[ks], dp);
-      }
+    for (int b = 0; b < 4; ++b) {
+      const f32x4_t ls = *reinterpret_cast<const f32x4_t*>(&stat[buf][0][32 * w + 8 * b + 4 * h]);
+      const f32x4_t dl = *reinterpret_cast<const f32x4_t*>(&stat[buf][1][32 * w + 8 * b + 4 * h]);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const f32x4_t ls = *reinterpret_cast<const f32x4_t*>(&stat[st & 1][0][32 * w + 8 * b + 4 * h]);
-        const f32x4_t dl = *reinterpret_cast<const f32x4_t*>(&stat[st & 1][1][32 * w + 8 * b + 4 * h]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 4 * b + i;
-          s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, -ls[i] * kLog2e));
-          dp[r] = s[r] * (dp[r] - dl[i]);
-        }
-      }
-      if (r0 < w0 + 31 || r0 + 32 > at.n) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int q = r0 + reg_row(r) + 4 * h;
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * b + i;
+        p.s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(p.s[r], c, -ls[i]));
+        p.dp[r] = p.s[r] * (p.dp[r] - dl[i]);
+        if constexpr (decltype(masked)::value) {
+          const int q = j * kTile + 32 * w + reg_row(r) + 4 * h;
           if (q < ki || q >= at.n) {
-            s[r] = 0.0f;
-            dp[r] = 0.0f;
+            p.s[r] = 0.0f;
+            p.dp[r] = 0.0f;
           }
         }
       }
+    }
+  };
+  auto gather = [&](int buf, int w, const Pair& p) __attribute__((always_inline)) {
+    const char* qt = lds[buf][0];
+    const char* gt = lds[buf][1];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const bf16x8_t pf = pack8(s, m), sf = pack8(dp, m);
+    for (int m = 0; m < 2; ++m) {
+      const bf16x8_t pf = pack8(p.s, m), sf = pack8(p.dp, m);
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-          const char* g = gt + 16 * m * D * 2;
-          const char* q = qt + 16 * m * D * 2;
-          av[dt] = mfma(read_tr(g + of.tr[dt][0], g + of.tr[dt][1]), pf, av[dt]);
-          ak[dt] = mfma(read_tr(q + of.tr[dt][0], q + of.tr[dt][1]), sf, ak[dt]);
-        }
+      for (int dt = 0; dt < DT; ++dt) {
+        av[dt] = mfma(read_tr<64>(gt, of, 2 * w + m, dt), pf, av[dt]);
+        ak[dt] = mfma(read_tr<64>(qt, of, 2 * w + m, dt), sf, ak[dt]);
       }
     }
-  }
+  };
+
+  // First the tiles that some key does not see whole (two on the diagonal,
+  // one that the sequence's end cuts), then all others: one kind of step a
+  // loop, so that the sums stay where they are.
+  const int edge = at.n % kTile && per > 2 ? 1 : 0, front = min(per, 2), inner = per - front - edge;
+  auto sweep = [&](int count, int first, auto masked) __attribute__((always_inline)) {
+    // `count` tiles a head: j0 + first .., the cut one last in the first sweep
+    int i = 0, k = 0;
+    auto tile_of = [&](int kk) { return decltype(masked)::value && kk == front ? j0 + per - 1 : j0 + first + kk; };
+    const int steps = count * G;
+    if (steps == 0) return;
+    copy_step(0, 0, tile_of(0));
+    for (int st = 0; st < steps; ++st) {
+      const int j = tile_of(k), buf = st & 1;
+      if (++k == count) {
+        k = 0;
+        ++i;
+      }
+      land();
+      if (st + 1 < steps) copy_step(buf ^ 1, i, tile_of(k));
+      Pair p0, p1;
+      scores(buf, 0, p0);
+      scores(buf, 1, p1);
+      weigh(buf, j, 0, p0, masked);
+      gather(buf, 0, p0);
+      weigh(buf, j, 1, p1, masked);
+      gather(buf, 1, p1);
+    }
+    land();                                                     // the tiles are free again
+  };
+  sweep(front + edge, 0, std::true_type{});
+  sweep(inner, front, std::false_type{});
   if (ki >= at.n) return;
+  if (parts > 1) {
+    const int64_t set = static_cast<int64_t>(a.T) * a.Hkv * D;
+    float* dst = part + 2 * pt * set + (t * a.Hkv + hk) * D + 4 * h;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        *reinterpret_cast<f32x4_t*>(dst + 32 * dt + 8 * b) = f32x4_t{ak[dt][4 * b], ak[dt][4 * b + 1], ak[dt][4 * b + 2], ak[dt][4 * b + 3]};
+        *reinterpret_cast<f32x4_t*>(dst + set + 32 * dt + 8 * b) = f32x4_t{av[dt][4 * b], av[dt][4 * b + 1], av[dt][4 * b + 2], av[dt][4 * b + 3]};
+      }
+    return;
+  }
   uint16_t* dk = gk + (t * a.Hkv + hk) * D + 4 * h;
   uint16_t* dv = gv + (t * a.Hkv + hk) * D + 4 * h;
 #pragma unroll
@@ -480,46 +624,87 @@ __global__ __launch_bounds__(256, 1) void k_prompt_bwd_kv(PromptArgs a, const ui
     }
 }
 
+// Adds the parts of grad_k and grad_v in order; rows outside every sequence
+// have none.  Four elements a thread.
+__global__ __launch_bounds__(256) void k_prompt_join(PromptArgs a, const float* __restrict__ part, int parts,
+                                                     uint16_t* __restrict__ gk, uint16_t* __restrict__ gv) {
+  const int first = min(max(a.offsets[0], 0), a.T), last = min(max(a.offsets[a.B], first), a.T);
+  const int64_t row = static_cast<int64_t>(a.Hkv) * a.D, set = a.T * row;
+  for (int64_t i = 4 * (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) + first * row; i < last * row;
+       i += static_cast<int64_t>(gridDim.x) * 1024) {
+    f32x4_t k = *reinterpret_cast<const f32x4_t*>(part + i), v = *reinterpret_cast<const f32x4_t*>(part + set + i);
+    for (int p = 1; p < parts; ++p) {
+      const f32x4_t x = *reinterpret_cast<const f32x4_t*>(part + 2 * p * set + i);
+      const f32x4_t y = *reinterpret_cast<const f32x4_t*>(part + (2 * p + 1) * set + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        k[e] += x[e];
+        v[e] += y[e];
+      }
+    }
+    *reinterpret_cast<uint2*>(gk + i) = make_uint2(pack_bf16x2(k[0] * a.scale, k[1] * a.scale), pack_bf16x2(k[2] * a.scale, k[3] * a.scale));
+    *reinterpret_cast<uint2*>(gv + i) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
+}
+
 // Most tiles that T rows in B sequences can make.
-int64_t tile_bound(const PromptArgs& a) { return a.T / kRows + a.B + 1; }
+int64_t tile_bound(int64_t T, int32_t B) { return T / kRows + B + 1; }
+
+// Floats of the rows' statistics, rounded up to 16 bytes.
+int64_t stat_floats(int64_t T, int32_t Hq) { return (2 * T * Hq + 3) / 4 * 4; }
+
+// Workgroups over which the heads of a group are split: as many as bring the
+// launch to one workgroup per compute unit.
+int head_parts(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int cus) {
+  const int64_t tiles = (T / kRows + 1) * Hkv;                  // of one sequence; more make more
+  const int64_t want = cus / tiles;
+  return static_cast<int>(want < 1 ? 1 : want > Hq / Hkv ? Hq / Hkv : want);
+}
 
 template <int D>
-hipError_t forward(const PromptArgs& a, void* out, float* lse, hipStream_t stream) {
-  const int bound = static_cast<int>(tile_bound(a));
-  k_prompt_fwd<D><<<static_cast<unsigned>(bound) * a.Hq, 256, 0, stream>>>(a, static_cast<uint16_t*>(out), lse, bound);
+hipError_t forward(const PromptArgs& a, void* out, void* rest, float* lse, hipStream_t stream) {
+  const int bound = static_cast<int>(tile_bound(a.T, a.B));
+  k_prompt_fwd<D><<<static_cast<unsigned>(bound) * a.Hq, 256, 0, stream>>>(a, static_cast<uint16_t*>(out),
+                                                                          static_cast<uint16_t*>(rest), lse, bound);
   return hipGetLastError();
 }
 
 template <int D>
-hipError_t backward(const PromptArgs& a, const void* grad_out, int64_t go_stride, const void* out, const float* lse,
-                    void* gq, void* gk, void* gv, void* ws, hipStream_t stream) {
-  const int bound = static_cast<int>(tile_bound(a));
-  float* delta = static_cast<float*>(ws);
-  const uint16_t* go = static_cast<const uint16_t*>(grad_out);
-  const int64_t groups = (static_cast<int64_t>(a.T) * a.Hq * (D / 8) + 255) / 256;
-  k_prompt_delta<D><<<static_cast<unsigned>(groups < 4096 ? groups : 4096), 256, 0, stream>>>(
-      a, go, go_stride, static_cast<const uint16_t*>(out), delta);
+hipError_t backward(const PromptArgs& a, const GradArgs& g, void* gq, void* gk, void* gv, hipStream_t stream) {
+  const int bound = static_cast<int>(tile_bound(a.T, a.B));
+  k_prompt_bwd_q<D><<<static_cast<unsigned>(bound) * a.Hq, 256, 0, stream>>>(a, g, static_cast<uint16_t*>(gq), bound);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_prompt_bwd_kv<D><<<static_cast<unsigned>(bound) * a.Hkv, 256, 0, stream>>>(
-      a, go, go_stride, lse, delta, static_cast<uint16_t*>(gk), static_cast<uint16_t*>(gv), bound);
+  const int parts = head_parts(a.T, a.B, a.Hq, a.Hkv, device_cu_count());
+  float* part = g.stat + stat_floats(a.T, a.Hq);
+  k_prompt_bwd_kv<D><<<static_cast<unsigned>(bound) * a.Hkv * parts, 256, 0, stream>>>(
+      a, g, static_cast<uint16_t*>(gk), static_cast<uint16_t*>(gv), part, parts, bound);
   e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  k_prompt_bwd_q<D><<<static_cast<unsigned>(bound) * a.Hq, 256, 0, stream>>>(a, go, go_stride, lse, delta,
-                                                                            static_cast<uint16_t*>(gq), bound);
+  if (e != hipSuccess || parts == 1) return e;
+  const int64_t groups = (static_cast<int64_t>(a.T) * a.Hkv * D / 4 + 255) / 256;
+  k_prompt_join<<<static_cast<unsigned>(groups < 2048 ? groups : 2048), 256, 0, stream>>>(
+      a, part, parts, static_cast<uint16_t*>(gk), static_cast<uint16_t*>(gv));
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_prompt_fwd(const PromptArgs& a, void* out, float* lse, hipStream_t stream) {
-  return a.D == 128 ? forward<128>(a, out, lse, stream) : forward<64>(a, out, lse, stream);
+hipError_t launch_prompt_fwd(const PromptArgs& a, void* out, void* rest, float* lse, hipStream_t stream) {
+  return a.D == 128 ? forward<128>(a, out, rest, lse, stream) : forward<64>(a, out, rest, lse, stream);
 }
 
 hipError_t launch_prompt_bwd(const PromptArgs& a, const void* grad_out, int64_t grad_stride, const void* out,
-                             const float* lse, void* grad_q, void* grad_k, void* grad_v, void* ws, hipStream_t stream) {
-  return a.D == 128 ? backward<128>(a, grad_out, grad_stride, out, lse, grad_q, grad_k, grad_v, ws, stream)
-                    : backward<64>(a, grad_out, grad_stride, out, lse, grad_q, grad_k, grad_v, ws, stream);
+                             const void* rest, const float* lse, void* grad_q, void* grad_k, void* grad_v, void* ws,
+                             hipStream_t stream) {
+  const GradArgs g{static_cast<const uint16_t*>(grad_out), static_cast<const uint16_t*>(out),
+                   static_cast<const uint16_t*>(rest), grad_stride, lse, static_cast<float*>(ws)};
+  return a.D == 128 ? backward<128>(a, g, grad_q, grad_k, grad_v, stream) : backward<64>(a, g, grad_q, grad_k, grad_v, stream);
+}
+
+size_t prompt_bwd_ws_bytes(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
+  const int parts = head_parts(T, B, Hq, Hkv, device_cu_count());
+  const int64_t sums = parts > 1 ? 2 * parts * T * Hkv * D : 0;
+  return static_cast<size_t>(stat_floats(T, Hq) + sums) * sizeof(float);
 }
 
 }  // namespace nf4

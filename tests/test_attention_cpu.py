@@ -114,11 +114,11 @@ def test_dequantize_refuses(lib):
 
 def test_prompt_refuses(lib):
     def fwd(q=A, qs=256, k=A, ks=128, v=A, vs=128, T=4, off=A, B=1, Hq=4, Hkv=2, D=64, scale=0.125, out=A, lse=A):
-        return lib.nf4_prompt_attention_fwd(q, qs, k, ks, v, vs, T, off, B, Hq, Hkv, D, scale, out, lse, 1, None)
+        return lib.nf4_prompt_attention_fwd(q, qs, k, ks, v, vs, T, off, B, Hq, Hkv, D, scale, out, None, lse, 1, None)
 
     def bwd(g=A, gs=256, q=A, k=A, v=A, out=A, lse=A, T=4, off=A, B=1, Hq=4, Hkv=2, D=64, scale=0.125, gq=A, gk=A, gv=A,
-            ws=A, wsb=1 << 20):
-        return lib.nf4_prompt_attention_bwd(g, gs, q, 256, k, 128, v, 128, out, lse, T, off, B, Hq, Hkv, D, scale, gq, gk,
+            ws=A, wsb=1 << 30):
+        return lib.nf4_prompt_attention_bwd(g, gs, q, 256, k, 128, v, 128, out, None, lse, T, off, B, Hq, Hkv, D, scale, gq, gk,
                                             gv, 1, ws, wsb, None)
     assert fwd(q=None) == fwd(k=None) == fwd(v=None) == fwd(off=None) == fwd(out=None) == L.NF4_ERR_NULL
     assert fwd(Hq=3) == fwd(T=-1) == fwd(ks=-8) == fwd(scale=0.0) == L.NF4_ERR_SHAPE
@@ -128,9 +128,9 @@ def test_prompt_refuses(lib):
     assert fwd(T=0, q=None, k=None, v=None, out=None, lse=None) == L.NF4_OK
     assert bwd(g=None) == bwd(out=None) == bwd(lse=None) == bwd(gq=None) == bwd(gk=None) == bwd(gv=None) == L.NF4_ERR_NULL
     assert bwd(gs=4) == bwd(gk=BAD) == bwd(ws=BAD) == L.NF4_ERR_ALIGN
-    assert bwd(ws=None) == bwd(wsb=lib.nf4_prompt_attention_bwd_workspace(4, 4) - 1) == L.NF4_ERR_WORKSPACE
+    assert bwd(ws=None) == bwd(wsb=lib.nf4_prompt_attention_bwd_workspace(4, 1, 4, 2, 64) - 1) == L.NF4_ERR_WORKSPACE
     assert bwd(T=0, g=None, q=None, k=None, v=None, out=None, lse=None, gq=None, gk=None, gv=None, ws=None) == L.NF4_OK
-    assert lib.nf4_prompt_attention_bwd_workspace(-1, 4) == BIG
+    assert lib.nf4_prompt_attention_bwd_workspace(-1, 1, 4, 2, 64) == BIG
 
 
 def test_python_refuses_host_tensors():

@@ -26,7 +26,7 @@ def test_forward(lens, D):
     joint, q, k, v = inputs(lens, Hq, Hkv, D, seed=sum(lens))
     jd = joint.to(DEV)                                          # rows of a joint projection, taken as they are
     off = R.offsets_of(lens).to(DEV)
-    out, lse = nf4_prompt_attention_fwd(jd[:, :Hq], jd[:, Hq:Hq + Hkv], jd[:, Hq + Hkv:], off, want_lse=True)
+    out, _, lse = nf4_prompt_attention_fwd(jd[:, :Hq], jd[:, Hq:Hq + Hkv], jd[:, Hq + Hkv:], off, for_backward=True)
     sc = float(np.float32(D ** -0.5))
     want, bound = R.prompt(q, k, v, lens, sc)["out"]
     R.within(out, want, bound, f"{lens}")
@@ -148,7 +148,7 @@ def test_rows_outside_sequences():
         assert not g[T:].any()
     assert not out[T:].any()
     mark = torch.full_like(out, 3.0).detach()
-    o2, _ = nf4_prompt_attention_fwd(*(x.detach() for x in leaves), off, out=mark)
+    o2 = nf4_prompt_attention_fwd(*(x.detach() for x in leaves), off, out=mark)
     assert torch.equal(o2[:T], out[:T]) and (o2[T:] == 3.0).all()
 
 
@@ -217,13 +217,13 @@ def test_repeatable_and_streams():
     off = R.offsets_of(lens).to(DEV)
     xs = [x.to(DEV).contiguous() for x in (q, k, v)]
     gy = R.normal(92, sum(lens), 8, 128).to(DEV)
-    out, lse = nf4_prompt_attention_fwd(*xs, off, want_lse=True)
-    ref = nf4_prompt_attention_bwd(gy, *xs, out, lse, off)
+    out, rest, lse = nf4_prompt_attention_fwd(*xs, off, for_backward=True)
+    ref = nf4_prompt_attention_bwd(gy, *xs, out, rest, lse, off)
     torch.cuda.synchronize()
     for s in (torch.cuda.Stream(), torch.cuda.Stream()):
         with torch.cuda.stream(s):
-            o, l = nf4_prompt_attention_fwd(*xs, off, want_lse=True)
-            g = nf4_prompt_attention_bwd(gy, *xs, o, l, off)
+            o, r, l = nf4_prompt_attention_fwd(*xs, off, for_backward=True)
+            g = nf4_prompt_attention_bwd(gy, *xs, o, r, l, off)
         torch.cuda.synchronize()
         assert torch.equal(o, out) and torch.equal(l, lse) and all(torch.equal(a, b) for a, b in zip(g, ref))
 
@@ -237,8 +237,8 @@ def test_graph_follows_the_offsets():
     off = torch.zeros(4, dtype=torch.int32, device=DEV)
 
     def step():
-        o, l = nf4_prompt_attention_fwd(*xs, off, want_lse=True)
-        return (o, *nf4_prompt_attention_bwd(gy, *xs, o, l, off))
+        o, r, l = nf4_prompt_attention_fwd(*xs, off, for_backward=True)
+        return (o, *nf4_prompt_attention_bwd(gy, *xs, o, r, l, off))
 
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -259,8 +259,8 @@ def test_path_counts_and_refusals():
     x = R.normal(1, 6, 2, 64).to(DEV)
     off = torch.tensor([0, 6], dtype=torch.int32, device=DEV)
     api.nf4_reset_path_counts()
-    out, lse = nf4_prompt_attention_fwd(x, x, x, off, want_lse=True)
-    nf4_prompt_attention_bwd(x, x, x, x, out, lse, off)
+    out, rest, lse = nf4_prompt_attention_fwd(x, x, x, off, for_backward=True)
+    nf4_prompt_attention_bwd(x, x, x, x, out, rest, lse, off)
     c = api.nf4_path_counts()
     assert (c["prompt_fwd"], c["prompt_bwd"]) == (1, 1)
 
@@ -279,6 +279,6 @@ def test_path_counts_and_refusals():
     bad(x, x, x, off, scale=-1.0)
     bad(x, x, x, off, out=x.float())
     with pytest.raises(ValueError):
-        nf4_prompt_attention_bwd(x, x, x, x, out, lse[:1], off)
+        nf4_prompt_attention_bwd(x, x, x, x, out, rest, lse[:1], off)
     with pytest.raises(RuntimeError):
-        nf4_prompt_attention_bwd(x, x, x, x, out, lse, off, ws=torch.empty(16, dtype=torch.uint8, device=DEV))
+        nf4_prompt_attention_bwd(x, x, x, x, out, rest, lse, off, ws=torch.empty(16, dtype=torch.uint8, device=DEV))
