@@ -71,6 +71,23 @@ hipError_t launch_prompt_bwd(const PromptArgs& a, const void* grad_out, int64_t 
 
 // ---- device helpers ----------------------------------------------------------
 
+// Copies straight into LDS, invisible to the compiler's own waits; the kernels
+// wait for them themselves.  The LDS address is uniform, lane i lands 16 i
+// (4 i) bytes behind it.
+typedef __attribute__((address_space(3))) void lds_ptr_t;
+__device__ __forceinline__ void copy16(uint32_t off, const char* base, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" :: "v"(off), "s"(base), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(src), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void copy4(const void* src, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" :: "v"(src), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_ptr_t*)p));
+}
+
 // Sum over the wave (the same in all lanes) and inclusive prefix sum, in the
 // vector unit's lane moves: rows of 16 lanes first, then across the rows.
 template <int CTRL, int ROWS>

@@ -8,12 +8,13 @@ namespace {
 
 constexpr float kDeadBlock = 7.52316384526264e-37f;   // 2^-120
 
+// Where a row lies in the cache.
 struct Place {
   int seq, pos;         // seq < 0: the row is outside every sequence
-  int64_t slot;         // page * page size + place, < 0: a hole
+  int64_t vec;          // (page * Hkv) * page size + place: head h adds h * page size; < 0: a hole
 };
 
-// Where row t lies in the cache (t is the same in the whole wave).
+// Place of row t (the same t in the whole wave).
 __device__ __forceinline__ Place place_of(const KVSeqs& s, const KVCache& c, int t) {
   Place p{seq_of(s.offsets, s.B, s.T, t), 0, -1};
   if (p.seq < 0) return p;
@@ -22,37 +23,30 @@ __device__ __forceinline__ Place place_of(const KVSeqs& s, const KVCache& c, int
   const int i = p.pos / c.page;
   if (p.pos >= 0 && i < s.width) {
     const int64_t pg = s.table[static_cast<int64_t>(p.seq) * s.width + i];
-    if (pg >= 0 && pg < c.P) p.slot = pg * c.page + p.pos % c.page;
+    if (pg >= 0 && pg < c.P) p.vec = pg * c.Hkv * c.page + (p.pos - i * c.page);
   }
   return p;
 }
 
-// Index of (slot, head) among the cache's vectors of D elements.
-__device__ __forceinline__ int64_t vec_of(const KVCache& c, int64_t slot, int h) {
-  const int64_t pg = slot / c.page;
-  return (pg * c.Hkv + h) * c.page + (slot - pg * c.page);
-}
-
 // ---- append ----------------------------------------------------------------
-// One workgroup takes `tt` consecutive rows and every `gridDim.y`-th head.  The
-// sines and cosines of its rows are computed once in 64 bits into LDS and
-// shared by all heads; a thread then turns 8 neighbouring elements, reading
-// their partners a second time (from cache), and the 8 threads of a block of
-// 64 agree on its largest magnitude.  Bound by memory: 2 bytes in per element
-// and 0.5 to 2.5 out.
-constexpr int kAppendRows = 16;
-
-__global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendArgs a, int tt) {
-  __shared__ double2 turn[kAppendRows * 64];
-  __shared__ int64_t slots[kAppendRows];
-  __shared__ int seqs[kAppendRows];
-  const int D = c.D, D8 = D / 8, half = a.half;
-  const int t0 = blockIdx.x * tt, rows = min(tt, s.T - t0);
+// One workgroup takes TT consecutive rows (and, with TT == 1, 256 * 8 elements
+// of them).  The sines and cosines of its rows are computed once in 64 bits into
+// LDS and shared by all heads; a thread then turns 8 neighbouring elements,
+// reading their partners a second time (from cache), and the 8 threads of a
+// block of 64 agree on its largest magnitude.  Bound by memory: 2 bytes in per
+// element and 0.5 to 2.5 out.
+template <int D, int TT>
+__global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendArgs a) {
+  constexpr int D8 = D / 8, kPer = TT * D8;
+  __shared__ double2 turn[TT * 64];
+  __shared__ int64_t vecs[TT];
+  __shared__ int seqs[TT];
+  const int half = a.half, t0 = blockIdx.x * TT, rows = min(TT, s.T - t0);
   for (int r = threadIdx.x >> 6; r < rows; r += 4) {
     const Place p = place_of(s, c, t0 + r);
     const int lane = threadIdx.x & 63;
     if (lane == 0) {
-      slots[r] = p.slot;
+      vecs[r] = p.vec;
       seqs[r] = p.seq;
     }
     if (p.seq >= 0 && lane < half) {
@@ -62,13 +56,10 @@ __global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendAr
     }
   }
   __syncthreads();
-  const int heads = (a.q ? a.Hq : 0) + 2 * c.Hkv, first_k = a.q ? a.Hq : 0;
-  const int per_head = rows * D8;
-  const int step = 256 * gridDim.y;
-  const int total = heads * per_head;                       // a multiple of 8
-  for (int i = blockIdx.y * 256 + threadIdx.x; i < total; i += step) {
-    const int hd = i / per_head, j = i - hd * per_head;
-    const int r = j / D8, e = 8 * (j - r * D8);
+  const int first_k = a.q ? a.Hq : 0, total = (first_k + 2 * c.Hkv) * kPer;
+  for (int i = blockIdx.y * 256 + threadIdx.x; i < total; i += 256 * gridDim.y) {
+    const int hd = i / kPer, r = i % kPer / D8, e = 8 * (i % D8);
+    if (r >= rows) continue;
     const int64_t t = t0 + r;
     const bool is_q = hd < first_k, is_v = hd >= first_k + c.Hkv;
     const int h = is_q ? hd : is_v ? hd - first_k - c.Hkv : hd - first_k;
@@ -95,16 +86,16 @@ __global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendAr
         const bool low = e < half;
         const uint4 wo = *reinterpret_cast<const uint4*>(src + (low ? e + half : e - half));
         const uint32_t o[4] = {wo.x, wo.y, wo.z, wo.w};
+        const uint32_t flip = low ? 0x80000000u : 0u;           // a c - b s below, b c + a s above
         const int f = low ? e : e - half;
         float z[8];
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
           const double2 cs = turn[r * 64 + f + p];
           const uint32_t mi = p & 1 ? x[p / 2] & 0xFFFF0000u : x[p / 2] << 16;
-          const uint32_t ot = p & 1 ? o[p / 2] & 0xFFFF0000u : o[p / 2] << 16;
-          const double m = static_cast<double>(__builtin_bit_cast(float, mi)) * cs.x;
-          const double n = static_cast<double>(__builtin_bit_cast(float, ot)) * cs.y;
-          z[p] = static_cast<float>(low ? m - n : m + n);
+          const uint32_t ot = (p & 1 ? o[p / 2] & 0xFFFF0000u : o[p / 2] << 16) ^ flip;
+          z[p] = static_cast<float>(static_cast<double>(__builtin_bit_cast(float, mi)) * cs.x +
+                                    static_cast<double>(__builtin_bit_cast(float, ot)) * cs.y);
         }
 #pragma unroll
         for (int p = 0; p < 4; ++p) x[p] = pack_bf16x2(z[2 * p], z[2 * p + 1]);
@@ -122,7 +113,8 @@ __global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendAr
     }
 #pragma unroll
     for (int d = 1; d < 8; d *= 2) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
-    if (slots[r] < 0) continue;
+    const int64_t base = vecs[r];
+    if (base < 0) continue;
     const float amax = __builtin_bit_cast(float, top << 16);
     const bool bad = top >= 0x7F80u, dead = amax < kDeadBlock;
     const float sc = bad ? __builtin_bit_cast(float, 0x7FC00000u) : dead ? 0.0f : amax / 6.0f;
@@ -145,7 +137,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendAr
         }
       }
     }
-    const int64_t vec = vec_of(c, slots[r], h);
+    const int64_t vec = base + h * c.page;
     *reinterpret_cast<uint32_t*>((is_v ? c.v_codes : c.k_codes) + vec * (D / 2) + e / 2) = code;
     if ((e & 63) == 0) (is_v ? c.v_scale : c.k_scale)[vec * (D / 64) + e / 64] = sc;
   }
@@ -153,36 +145,36 @@ __global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendAr
 
 // ---- read back ---------------------------------------------------------------
 // 8 elements a thread: one dword of patterns, four hardware conversions.
-__global__ __launch_bounds__(256) void k_kv_dequantize(KVCache c, KVSeqs s, uint16_t* k_out, uint16_t* v_out, int fill,
-                                                       int tt) {
-  __shared__ int64_t slots[kAppendRows];
-  __shared__ int seqs[kAppendRows];
-  const int D = c.D, D8 = D / 8;
-  const int t0 = blockIdx.x * tt, rows = min(tt, s.T - t0);
+template <int D, int TT>
+__global__ __launch_bounds__(256) void k_kv_dequantize(KVCache c, KVSeqs s, uint16_t* k_out, uint16_t* v_out, int fill) {
+  constexpr int D8 = D / 8, kPer = TT * D8;
+  __shared__ int64_t vecs[TT];
+  __shared__ int seqs[TT];
+  const int t0 = blockIdx.x * TT, rows = min(TT, s.T - t0);
   for (int r = threadIdx.x >> 6; r < rows; r += 4) {
     const Place p = place_of(s, c, t0 + r);
     if ((threadIdx.x & 63) == 0) {
-      slots[r] = p.slot;
+      vecs[r] = p.vec;
       seqs[r] = p.seq;
     }
   }
   __syncthreads();
-  const int per_head = rows * D8, total = 2 * c.Hkv * per_head;
+  const int total = 2 * c.Hkv * kPer;
   for (int i = blockIdx.y * 256 + threadIdx.x; i < total; i += 256 * gridDim.y) {
-    const int hd = i / per_head, j = i - hd * per_head;
-    const int r = j / D8, e = 8 * (j - r * D8);
+    const int hd = i / kPer, r = i % kPer / D8, e = 8 * (i % D8);
+    if (r >= rows || (seqs[r] < 0 && !fill)) continue;
     const bool is_v = hd >= c.Hkv;
     const int h = is_v ? hd - c.Hkv : hd;
-    if (seqs[r] < 0 && !fill) continue;
     uint32_t x[4] = {0u, 0u, 0u, 0u};
-    if (slots[r] >= 0) {
-      const int64_t vec = vec_of(c, slots[r], h);
+    const int64_t base = vecs[r];
+    if (base >= 0) {
+      const int64_t vec = base + h * c.page;
       const uint32_t code = *reinterpret_cast<const uint32_t*>((is_v ? c.v_codes : c.k_codes) + vec * (D / 2) + e / 2);
       const float sc = (is_v ? c.v_scale : c.k_scale)[vec * (D / 64) + e / 64];
-      bf16x2_t l[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, 1.0f, 0),
-                       __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, 1.0f, 1),
-                       __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, 1.0f, 2),
-                       __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, 1.0f, 3)};
+      const bf16x2_t l[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, 1.0f, 0),
+                             __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, 1.0f, 1),
+                             __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, 1.0f, 2),
+                             __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, 1.0f, 3)};
 #pragma unroll
       for (int p = 0; p < 4; ++p)
         x[p] = pack_bf16x2(static_cast<float>(l[p][1]) * sc, static_cast<float>(l[p][0]) * sc);
@@ -202,6 +194,7 @@ __global__ __launch_bounds__(256) void k_kv_dequantize(KVCache c, KVSeqs s, uint
 // scale of a block multiplies the fp32 partial score (keys) or the weight
 // (values), never an element.
 constexpr int kStep = 128;           // tokens per workgroup step, 32 a wave
+constexpr float kSlack = 8.0f;       // see the running maximum below
 
 template <int D, int MT>
 struct KVPart {                       // one worker's partial result of a unit
@@ -224,29 +217,39 @@ __device__ __forceinline__ SeqInfo seq_info(const KVSeqs& s, int b, int G, int c
   return i;
 }
 
-// Steps of the whole call, and the steps each worker takes.
+// Steps of the whole call, those of the sequences before `upto`, and the steps
+// each worker takes.
 template <int MT>
-__device__ __forceinline__ void share(const KVSeqs& s, int Hkv, int G, int cap, int workers, int& total, int& per) {
-  int sum = 0;
-  for (int b0 = 0; b0 < s.B; b0 += 64) {
-    const int b = b0 + (threadIdx.x & 63);
-    if (b < s.B) {
-      const SeqInfo i = seq_info<MT>(s, b, G, cap);
-      sum += Hkv * i.tiles * i.steps;
-    }
+__device__ __forceinline__ void share(const KVSeqs& s, int Hkv, int G, int cap, int workers, int upto, int& total,
+                                      int& before, int& per) {
+  int sum = 0, pre = 0;
+  for (int b = threadIdx.x & 63; b < s.B; b += 64) {
+    const SeqInfo i = seq_info<MT>(s, b, G, cap);
+    const int st = Hkv * i.tiles * i.steps;
+    sum += st;
+    if (b < upto) pre += st;
   }
-  total = uniform(wave_sum(sum));
+  total = wave_sum(sum);
+  before = wave_sum(pre);
   per = max(1, (total + workers - 1) / workers);
 }
 
-template <int NB>
-struct KVTile {                       // what one wave reads of 32 tokens
-  uint2 k[2][NB];
-  f32x4_t ks[2][NB];
-  uint32_t v[2][NB][4];
-  f32x4_t vs[2][NB];
-  int ok;                             // bit u: 16-token tile u lies in a page
+// What one wave reads of 32 tokens, in LDS: the patterns of keys and values as
+// they lie in their pages ([2 tiles][16 tokens][D / 2]) and the scales ([2][16]
+// [D / 64]).  Each wave keeps kRing of these tiles, kRing - 1 on their way
+// while it works on one, and copies only for itself: no barriers.
+constexpr int kRing = 4;
+template <int D>
+struct KVTile {
+  static constexpr int kCopies = D == 128 ? 6 : 3;              // copy instructions a tile
+  uint8_t k[2][16 * D / 2], v[2][16 * D / 2];
+  float ks[2][16 * D / 64], vs[2][16 * D / 64];
 };
+
+template <int N>
+__device__ __forceinline__ void landed() {                     // all but this wave's last N copies
+  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
+}
 
 __device__ __forceinline__ bf16x8_t fp4_to_frag(uint32_t c) {
   const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, 1.0f, 0));
@@ -257,16 +260,19 @@ __device__ __forceinline__ bf16x8_t fp4_to_frag(uint32_t c) {
 }
 
 template <int D, int MT>
-__global__ __launch_bounds__(256) void k_kv_attention(KVCache c, KVSeqs s, const uint16_t* __restrict__ q,
+__global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_kv_attention(KVCache c, KVSeqs s, const uint16_t* __restrict__ q,
                                                       int64_t q_stride, int Hq, float scale2,
                                                       uint16_t* __restrict__ out, float* __restrict__ ws) {
-  constexpr int NB = D / 64, R = 16 * MT;
-  __shared__ __align__(16) float lds[2 * (R * D + 2 * R)];
+  constexpr int NB = D / 64, R = 16 * MT, kCopies = KVTile<D>::kCopies;
+  // the ring, and between segments the waves' results
+  constexpr size_t kRingBytes = 4 * kRing * sizeof(KVTile<D>), kJoinBytes = 2 * (R * D + 2 * R) * sizeof(float);
+  __shared__ __align__(1024) char shared[kRingBytes > kJoinBytes ? kRingBytes : kJoinBytes];
+  float* const lds = reinterpret_cast<float*>(shared);
   const int G = Hq / c.Hkv, cap = s.width * c.page;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  int total, per;
-  share<MT>(s, c.Hkv, G, cap, gridDim.x, total, per);
+  int total, none, per;
+  share<MT>(s, c.Hkv, G, cap, gridDim.x, 0, total, none, per);
   int lo = min(static_cast<int64_t>(total), static_cast<int64_t>(blockIdx.x) * per);
   const int hi = min(total, lo + per);
   if (lo >= hi) return;
@@ -307,7 +313,9 @@ __global__ __launch_bounds__(256) void k_kv_attention(KVCache c, KVSeqs s, const
     }
     const int u = (lo - base) / ns, s0 = lo - base - u * ns, s1 = min(ns, s0 + (hi - lo));
     const int rt = u / c.Hkv, h = u - rt * c.Hkv;
-    const int32_t* pt = s.table + static_cast<int64_t>(b) * s.width;
+    // read by the scalar unit: nothing writes the table while the kernel runs
+    typedef const __attribute__((address_space(4))) int32_t table_t;
+    table_t* pt = (table_t*)(s.table + static_cast<int64_t>(b) * s.width);
     const int seen = min(max(len, 0), cap);
 
     // queries: row rt * R + 16 mt + (lane & 15), elements 16 g .. of each block, pairs swapped as the conversion
@@ -346,142 +354,204 @@ __global__ __launch_bounds__(256) void k_kv_attention(KVCache c, KVSeqs s, const
         for (int x = 0; x < 4; ++x) acc[m][nb][x] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
 
-    auto fetch = [&](int step, KVTile<NB>& t) __attribute__((always_inline)) {
-      t.ok = 0;
+    // The wave's walk over the page table: index and place in the page of its
+    // two 16-token tiles, and the pages read one step ahead of their use.
+    KVTile<D>* const ring = reinterpret_cast<KVTile<D>*>(shared) + kRing * wave;
+    int pi[2], po[2], ids[2], at = s0 * kStep + 32 * wave;
+    const int page_q = kStep / c.page, page_r = kStep - page_q * c.page;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      pi[w] = (at + 16 * w) / c.page;
+      po[w] = at + 16 * w - pi[w] * c.page;
+    }
+    auto look_up = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) ids[w] = at + 16 * w < seen ? pt[pi[w]] : -1;
+    };
+    uint32_t oks = 0;                              // bit 2 k + w: tile w of the step k steps back lies in a page
+    auto fetch = [&](int slot) __attribute__((always_inline)) {
+      oks <<= 2;
+      int64_t vec[2];
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        const int t0 = step * kStep + 32 * wave + 16 * w;
-        int64_t pg = -1;
-        if (t0 < seen) pg = pt[t0 / c.page];
+        int64_t pg = ids[w];
         const bool ok = pg >= 0 && pg < c.P;
-        t.ok |= static_cast<int>(ok) << w;
+        oks |= static_cast<uint32_t>(ok) << w;
         if (!ok) pg = 0;                           // any page: its tokens are not seen
-        const int64_t vec = (pg * c.Hkv + h) * c.page + t0 % c.page;
-        const uint8_t* kc = c.k_codes + vec * (D / 2) + r16 * (D / 2) + 8 * g;
-        const uint8_t* vc = c.v_codes + vec * (D / 2) + (4 * g) * (D / 2) + 4 * (r16 & 7);
-        const float* ks = c.k_scale + (vec + 4 * g) * NB;
-        const float* vs = c.v_scale + (vec + 4 * g) * NB;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          t.k[w][nb] = *reinterpret_cast<const uint2*>(kc + 32 * nb);
-          t.ks[w][nb] = *reinterpret_cast<const f32x4_t*>(ks + 4 * nb);
-          t.vs[w][nb] = *reinterpret_cast<const f32x4_t*>(vs + 4 * nb);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) t.v[w][nb][i] = *reinterpret_cast<const uint32_t*>(vc + i * (D / 2) + 32 * nb);
+        vec[w] = (pg * c.Hkv + h) * c.page + po[w];
+        pi[w] += page_q;
+        po[w] += page_r;
+        if (po[w] >= c.page) {
+          po[w] -= c.page;
+          ++pi[w];
         }
       }
-    };
-    // scale of token 4g + i, block nb: floats [token][block]
-    auto scale_of = [](const f32x4_t (&sv)[NB], int i, int nb) __attribute__((always_inline)) {
-      return NB == 1 ? sv[0][i] : sv[(2 * i + nb) >> 2][(2 * i + nb) & 3];
+      at += kStep;
+      KVTile<D>& t = ring[slot];
+      const uint32_t l16 = 16 * lane;
+      const int64_t mine = lane < 32 ? vec[0] : vec[1];
+      if constexpr (D == 128) {                    // 16 tokens' patterns are 1024 bytes, their scales 128
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          copy16(l16, reinterpret_cast<const char*>(c.k_codes) + vec[w] * 64, lds_addr(t.k[w]));
+          copy16(l16, reinterpret_cast<const char*>(c.v_codes) + vec[w] * 64, lds_addr(t.v[w]));
+        }
+        copy4(c.k_scale + mine * 2 + (lane & 31), lds_addr(t.ks));
+        copy4(c.v_scale + mine * 2 + (lane & 31), lds_addr(t.vs));
+      } else {                                     // 512 and 64 bytes
+        copy16(c.k_codes + mine * 32 + 16 * (lane & 31), lds_addr(t.k));
+        copy16(c.v_codes + mine * 32 + 16 * (lane & 31), lds_addr(t.v));
+        const int64_t other = (lane & 16) ? vec[1] : vec[0];
+        copy4((lane < 32 ? c.k_scale : c.v_scale) + other + (lane & 15), lds_addr(t.ks));
+      }
     };
 
-    auto step_of = [&](int step, const KVTile<NB>& t) __attribute__((always_inline)) {
+    auto step_of = [&](int step, int slot, uint32_t ok) __attribute__((always_inline)) {
+      const KVTile<D>& t = ring[slot];
       const int t0 = step * kStep + 32 * wave;
-      // value patterns -> operands: bytes of 4 tokens together, then the two
-      // 16-token tiles' patterns into one byte
-      bf16x8_t vf[NB][4];
+      auto scale_of = [](const f32x4_t (&sv)[NB], int i, int nb) __attribute__((always_inline)) {
+        return NB == 1 ? sv[0][i] : sv[(2 * i + nb) >> 2][(2 * i + nb) & 3];
+      };
+      const bool whole = ok == 3 && t0 + 31 <= low;
+      float p[MT][2][4];
+      {
+        bf16x8_t kf[2][NB][2];
+        f32x4_t ks[2][NB];                         // scales of tokens 4g .. 4g+3: floats [token][block]
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        uint32_t y[2][2];
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const uint32_t a = perm(t.v[w][nb][1], t.v[w][nb][0], sel), d = perm(t.v[w][nb][3], t.v[w][nb][2], sel);
-          y[w][0] = perm(d, a, 0x05040100u);
-          y[w][1] = perm(d, a, 0x07060302u);
-        }
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          vf[nb][2 * p] = fp4_to_frag(bitsel(0x0F0F0F0Fu, y[0][p] >> 4, y[1][p]));
-          vf[nb][2 * p + 1] = fp4_to_frag(bitsel(0x0F0F0F0Fu, y[0][p], y[1][p] << 4));
-        }
-      }
-      bf16x8_t kf[2][NB][2];
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          kf[w][nb][0] = fp4_to_frag(t.k[w][nb].x);
-          kf[w][nb][1] = fp4_to_frag(t.k[w][nb].y);
-        }
-      const bool whole = t.ok == 3 && t0 + 31 <= low;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        float p[2][4];
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          f32x4_t d[NB];
+        for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            d[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[w][nb][0], qf[m][nb][0], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-            d[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[w][nb][1], qf[m][nb][1], d[nb], 0, 0, 0);
+            const uint2 x = *reinterpret_cast<const uint2*>(&t.k[w][r16 * (D / 2) + 8 * g + 32 * nb]);
+            ks[w][nb] = *reinterpret_cast<const f32x4_t*>(&t.ks[w][4 * g * NB + 4 * nb]);
+            kf[w][nb][0] = fp4_to_frag(x.x);
+            kf[w][nb][1] = fp4_to_frag(x.y);
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float x = d[0][i] * scale_of(t.ks[w], i, 0);
-            if constexpr (NB == 2) x = __builtin_fmaf(d[1][i], scale_of(t.ks[w], i, 1), x);
-            p[w][i] = x * scale2;
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            f32x4_t d[NB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              d[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[w][nb][0], qf[m][nb][0], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+              d[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[w][nb][1], qf[m][nb][1], d[nb], 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              p[m][w][i] = d[0][i] * scale_of(ks[w], i, 0);
+              if constexpr (NB == 2) p[m][w][i] = __builtin_fmaf(d[1][i], scale_of(ks[w], i, 1), p[m][w][i]);
+            }
           }
-        }
+      }
+      // keys first, then values: the operands of both at once would not fit
+      if constexpr (MT > 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
         if (!whole) {
 #pragma unroll
           for (int w = 0; w < 2; ++w)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              p[w][i] = ((t.ok >> w) & 1) && t0 + 16 * w + 4 * g + i <= lim[m] ? p[w][i] : -INFINITY;
+              p[m][w][i] = ((ok >> w) & 1) && t0 + 16 * w + 4 * g + i <= lim[m] ? p[m][w][i] : -INFINITY;
         }
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top = fmaxf(top, p[w][i]);
-        top = fmaxf(quad_max(top), mx[m]);
-        const float ref = top == -INFINITY ? 0.0f : top;
-        if (__any(top != mx[m])) {
-          const float f = __builtin_amdgcn_exp2f(mx[m] - ref);
+        float top = fmaxf(fmaxf(fmaxf(p[m][0][0], p[m][0][1]), p[m][0][2]), fmaxf(fmaxf(p[m][0][3], p[m][1][0]), p[m][1][1]));
+        top = quad_max(fmaxf(fmaxf(top, p[m][1][2]), p[m][1][3])) * scale2;
+        // the maximum in use moves only when a score passes it by 2^kSlack
+        if (__any(top > mx[m] + kSlack)) {
+          const float to = fmaxf(top, mx[m]), f = to == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[m] - to);
           sum[m] *= f;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int x = 0; x < 4; ++x) acc[m][nb][x] *= f;
-          mx[m] = top;
+          mx[m] = to;
         }
-        float ps = 0.0f;
+        const float ref = mx[m] == -INFINITY ? 0.0f : mx[m];
+        float ps[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            p[w][i] = __builtin_amdgcn_exp2f(p[w][i] - ref);
-            ps += p[w][i];
+            p[m][w][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[m][w][i], scale2, -ref));
+            ps[w] += p[m][w][i];
           }
-        sum[m] += ps;                              // this lane's tokens; the lanes of a row are added at the end
+        sum[m] += ps[0] + ps[1];                   // this lane's tokens; the lanes of a row are added at the end
+      }
+      f32x4_t vs[2][NB];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) vs[w][nb] = *reinterpret_cast<const f32x4_t*>(&t.vs[w][4 * g * NB + 4 * nb]);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        // value patterns -> operands: bytes of 4 tokens together, then the two
+        // 16-token tiles' patterns into one byte
+        bf16x8_t vf[4];
+        uint32_t y[2][2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          uint32_t x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = *reinterpret_cast<const uint32_t*>(&t.v[w][(4 * g + i) * (D / 2) + 4 * (r16 & 7) + 32 * nb]);
+          const uint32_t lo4 = perm(x[1], x[0], sel), hi4 = perm(x[3], x[2], sel);
+          y[w][0] = perm(hi4, lo4, 0x05040100u);
+          y[w][1] = perm(hi4, lo4, 0x07060302u);
+        }
+#pragma unroll
+        for (int b2 = 0; b2 < 2; ++b2) {
+          vf[2 * b2] = fp4_to_frag(bitsel(0x0F0F0F0Fu, y[0][b2] >> 4, y[1][b2]));
+          vf[2 * b2 + 1] = fp4_to_frag(bitsel(0x0F0F0F0Fu, y[0][b2], y[1][b2] << 4));
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
           float x[2][4];
 #pragma unroll
           for (int w = 0; w < 2; ++w)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[w][i] = p[w][i] * scale_of(t.vs[w], i, nb);
-              // an unseen token's scale may be anything
-              if (!whole)
-                x[w][i] = ((t.ok >> w) & 1) && t0 + 16 * w + 4 * g + i <= lim[m] ? x[w][i] : 0.0f;
-            }
+            for (int i = 0; i < 4; ++i) x[w][i] = p[m][w][i] * scale_of(vs[w], i, nb);
+          if (!whole) {                            // an unseen token's scale may be anything
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                x[w][i] = ((ok >> w) & 1) && t0 + 16 * w + 4 * g + i <= lim[m] ? x[w][i] : 0.0f;
+          }
           // rounded to bf16 for the matrix product: half a step of 2^-8 per weight
           const u32x4_t pw = {pack_bf16x2(x[0][0], x[1][0]), pack_bf16x2(x[0][1], x[1][1]),
                               pack_bf16x2(x[0][2], x[1][2]), pack_bf16x2(x[0][3], x[1][3])};
           const bf16x8_t pf = __builtin_bit_cast(bf16x8_t, pw);
 #pragma unroll
           for (int x4 = 0; x4 < 4; ++x4)
-            acc[m][nb][x4] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[nb][x4], pf, acc[m][nb][x4], 0, 0, 0);
+            acc[m][nb][x4] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[x4], pf, acc[m][nb][x4], 0, 0, 0);
         }
       }
     };
 
-    KVTile<NB> ta;
-    for (int st = s0; st < s1; ++st) {
-      fetch(st, ta);
-      step_of(st, ta);
+    look_up();
+    // fill the ring, then one tile in for each one worked on
+    for (int k = 0; k < kRing - 1 && s0 + k < s1; ++k) {
+      fetch(k);
+      look_up();
+    }
+    for (int st = s0, slot = 0; st < s1; ++st, slot = (slot + 1) % kRing) {
+      // the slot that is filled next was read to the end in the last step
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      const int left = s1 - 1 - st;                              // tiles behind this one
+      if (left >= kRing - 1) {
+        fetch((slot + kRing - 1) % kRing);
+        look_up();
+        landed<(kRing - 1) * kCopies>();
+      } else if (left == 2) {
+        landed<2 * kCopies>();
+      } else if (left == 1) {
+        landed<kCopies>();
+      } else {
+        landed<0>();
+      }
+      const int back = min(left, kRing - 1);                     // steps fetched behind this one
+      const uint32_t ok = (oks >> (2 * back)) & 3;
+      if (ok) step_of(st, slot, ok);
     }
 
     // join the four waves through LDS, two at a time
@@ -491,7 +561,7 @@ __global__ __launch_bounds__(256) void k_kv_attention(KVCache c, KVSeqs s, const
     float* const half_ms = lds + 2 * R * D;                        // [2][2][R]
 #pragma unroll
     for (int m = 0; m < MT; ++m) sum[m] = quad_sum(sum[m]);
-    for (int round = 0; round < 2; ++round) {
+    for (int round = 0; round < 2; ++round) {                      // (the ring is read to its end)
       const int senders = round == 0 ? 2 : 1;                      // waves 2, 3 -> 0, 1; then 1 -> 0
       __syncthreads();
       if (wave >= senders && wave < 2 * senders) {
@@ -575,6 +645,7 @@ __global__ __launch_bounds__(256) void k_kv_attention(KVCache c, KVSeqs s, const
       }
     }
     lo += s1 - s0;
+    __syncthreads();                                               // the results are read before the ring is filled again
   }
 }
 
@@ -588,20 +659,13 @@ __global__ __launch_bounds__(256) void k_kv_join(KVCache c, KVSeqs s, int Hq, ui
   __shared__ float red[NG][D + 4];
   const int G = Hq / c.Hkv, cap = s.width * c.page, t = blockIdx.x, hq = blockIdx.y;
   uint16_t* dst = out + (static_cast<int64_t>(t) * Hq + hq) * D;
-  const int lane = threadIdx.x & 63;
   const int bb = uniform(seq_of(s.offsets, s.B, s.T, t));
   if (bb < 0) {
     if (fill && threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(dst)[threadIdx.x] = 0u;
     return;
   }
-  int total, per;
-  share<MT>(s, c.Hkv, G, cap, workers, total, per);
-  int before = 0;
-  for (int b = lane; b < bb; b += 64) {
-    const SeqInfo i = seq_info<MT>(s, b, G, cap);
-    before += c.Hkv * i.tiles * i.steps;
-  }
-  before = uniform(wave_sum(before));
+  int total, before, per;
+  share<MT>(s, c.Hkv, G, cap, workers, bb, total, before, per);
   const SeqInfo si = seq_info<MT>(s, bb, G, cap);
   if (si.steps == 0) {
     if (threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(dst)[threadIdx.x] = 0u;
@@ -614,16 +678,28 @@ __global__ __launch_bounds__(256) void k_kv_join(KVCache c, KVSeqs s, int Hq, ui
   const int grp = threadIdx.x / LP, e = 4 * (threadIdx.x % LP);
   float m = -INFINITY, l = 0.0f;
   f32x4_t a = {0.f, 0.f, 0.f, 0.f};
-  for (int w = w0 + grp; w <= w1; w += NG) {
-    const float* part = ws + (2 * static_cast<size_t>(w) + (w * per >= u0 ? 0 : 1)) * KVPart<D, MT>::kFloats;
-    const float om = part[R * D + rr], os = part[R * D + R + rr];
-    const f32x4_t o = *reinterpret_cast<const f32x4_t*>(part + rr * D + e);
-    const float top = fmaxf(m, om), ref = top == -INFINITY ? 0.0f : top;
-    const float fa = __builtin_amdgcn_exp2f(m - ref), fb = __builtin_amdgcn_exp2f(om - ref);
-    m = top;
-    l = l * fa + os * fb;
+  constexpr int kAhead = 4;                                  // partial results asked for at once
+  for (int w = w0 + grp; w <= w1; w += kAhead * NG) {
+    float om[kAhead], os[kAhead];
+    f32x4_t o[kAhead];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) a[x] = a[x] * fa + o[x] * fb;
+    for (int k = 0; k < kAhead; ++k) {
+      const int wk = w + k * NG, wr = min(wk, w1);           // the last one again behind the end, unused
+      const float* part = ws + (2 * static_cast<size_t>(wr) + (wr * per >= u0 ? 0 : 1)) * KVPart<D, MT>::kFloats;
+      om[k] = part[R * D + rr];
+      os[k] = part[R * D + R + rr];
+      o[k] = *reinterpret_cast<const f32x4_t*>(part + rr * D + e);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (w + k * NG > w1) break;
+      const float top = fmaxf(m, om[k]), ref = top == -INFINITY ? 0.0f : top;
+      const float fa = __builtin_amdgcn_exp2f(m - ref), fb = __builtin_amdgcn_exp2f(om[k] - ref);
+      m = top;
+      l = l * fa + os[k] * fb;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) a[x] = a[x] * fa + o[k][x] * fb;
+    }
   }
   *reinterpret_cast<f32x4_t*>(&red[grp][e]) = a;
   if (e == 0) {
@@ -664,21 +740,42 @@ hipError_t attend(const KVAttnPlan& pl, const KVCache& c, const KVSeqs& s, const
 
 }  // namespace
 
+// Rows per workgroup: 16, so that the scales of neighbouring tokens share a
+// cache line in one workgroup's writes, where that still makes a workgroup per
+// compute unit; 1, spread over several workgroups, where there are few rows.
+int rows_per_group(int64_t T) { return T >= 4096 ? 16 : T >= 1024 ? 4 : 1; }
+
 hipError_t launch_kv_append(const KVCache& c, const KVSeqs& s, const AppendArgs& a, hipStream_t stream) {
-  const int tt = s.T >= 4096 ? kAppendRows : s.T >= 1024 ? 4 : 1;
-  const int64_t items = static_cast<int64_t>((a.q ? a.Hq : 0) + 2 * c.Hkv) * tt * (c.D / 8);
-  const int split = tt == 1 ? static_cast<int>((items + 255) / 256) : 1;
-  k_kv_append<<<dim3((s.T + tt - 1) / tt, split), 256, 0, stream>>>(c, s, a, tt);
+  const int tt = rows_per_group(s.T);
+  const int64_t items = static_cast<int64_t>((a.q ? a.Hq : 0) + 2 * c.Hkv) * (c.D / 8);
+  const dim3 grid((s.T + tt - 1) / tt, tt == 1 ? static_cast<unsigned>((items + 255) / 256) : 1);
+#define NF4_APPEND(D_, TT_) \
+  if (c.D == D_ && tt == TT_) k_kv_append<D_, TT_><<<grid, 256, 0, stream>>>(c, s, a)
+  NF4_APPEND(64, 1);
+  NF4_APPEND(64, 4);
+  NF4_APPEND(64, 16);
+  NF4_APPEND(128, 1);
+  NF4_APPEND(128, 4);
+  NF4_APPEND(128, 16);
+#undef NF4_APPEND
   return hipGetLastError();
 }
 
 hipError_t launch_kv_dequantize(const KVCache& c, const KVSeqs& s, void* k_out, void* v_out, int fill,
                                 hipStream_t stream) {
-  const int tt = s.T >= 4096 ? kAppendRows : s.T >= 1024 ? 4 : 1;
-  const int64_t items = static_cast<int64_t>(2 * c.Hkv) * tt * (c.D / 8);
-  const int split = tt == 1 ? static_cast<int>((items + 255) / 256) : 1;
-  k_kv_dequantize<<<dim3((s.T + tt - 1) / tt, split), 256, 0, stream>>>(c, s, static_cast<uint16_t*>(k_out),
-                                                                        static_cast<uint16_t*>(v_out), fill, tt);
+  const int tt = rows_per_group(s.T);
+  const int64_t items = static_cast<int64_t>(2 * c.Hkv) * (c.D / 8);
+  const dim3 grid((s.T + tt - 1) / tt, tt == 1 ? static_cast<unsigned>((items + 255) / 256) : 1);
+  uint16_t *k = static_cast<uint16_t*>(k_out), *v = static_cast<uint16_t*>(v_out);
+#define NF4_DEQUANTIZE(D_, TT_) \
+  if (c.D == D_ && tt == TT_) k_kv_dequantize<D_, TT_><<<grid, 256, 0, stream>>>(c, s, k, v, fill)
+  NF4_DEQUANTIZE(64, 1);
+  NF4_DEQUANTIZE(64, 4);
+  NF4_DEQUANTIZE(64, 16);
+  NF4_DEQUANTIZE(128, 1);
+  NF4_DEQUANTIZE(128, 4);
+  NF4_DEQUANTIZE(128, 16);
+#undef NF4_DEQUANTIZE
   return hipGetLastError();
 }
 

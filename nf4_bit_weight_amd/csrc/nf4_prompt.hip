@@ -18,61 +18,43 @@ namespace nf4 {
 namespace {
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
 
 constexpr int kTile = 64;       // streamed rows per step
 constexpr int kRows = 128;      // register rows per workgroup (32 a wave)
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-// Copies straight into LDS, invisible to the compiler's own waits; the kernel
-// waits for them itself (land).  The LDS address is uniform, lane i lands
-// 16 i (4 i) bytes behind it.
-__device__ __forceinline__ void dma_b128(uint32_t off, const char* base, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" :: "v"(off), "s"(base), "{m0}"(lds) : "memory");
-}
-__device__ __forceinline__ void dma_b32(const void* src, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" :: "v"(src), "{m0}"(lds) : "memory");
-}
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_void_t*)p));
-}
-// All but this wave's last N copies have landed, and every wave is here.
-template <int N = 0>
-__device__ __forceinline__ void land() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"(N) : "memory");
+__device__ __forceinline__ void land() {                       // every copy has landed, for every wave
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
-// LDS tile of TR rows (64 or 32): [D / 32 slices of 32 elements][TR rows][64
-// bytes], the 16-byte chunk c of a row's slice at chunk c ^ ((row >> 2) & 3).
+// LDS tile of 64 rows: [D / 32 slices of 32 elements][64 rows][64 bytes], the 16-byte chunk c of a row's slice at chunk c ^ ((row >> 2) & 3).
 // Both reads are free of bank conflicts (16 bytes of 8 neighbouring rows; the
 // transposed read's 32 bytes of 8 rows), and slice and row are immediate offsets
 // from two lane addresses each.
 //
-// Copier copies rows row0 .. row0+TR-1 of a sequence of n rows (the last row
-// again behind the end; its scores are masked) into such a tile: 16 rows of
-// one slice an instruction, kCopies instructions a wave.
-template <int D, int TR>
+// Copier copies rows row0 .. row0+63 of a sequence of n rows (the last row
+// again behind the end; its scores are masked) into such a tile: a wave copies
+// 16 rows, one slice an instruction.
+constexpr int kSlice = kTile * 64;                              // bytes
+template <int D>
 struct Copier {
-  static constexpr int kCopies = D / 32 * TR / 64;
   uint32_t off, stride;                                         // bytes
   int row;
   __device__ __forceinline__ explicit Copier(int64_t stride_elems) {
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    row = 16 * (TR == 64 ? wave : wave & 1) + (lane >> 2);
+    const int lane = threadIdx.x & 63;
+    row = 16 * uniform(threadIdx.x >> 6) + (lane >> 2);
     stride = static_cast<uint32_t>(stride_elems) * 2;
     off = 16 * ((lane & 3) ^ ((row >> 2) & 3));
   }
   __device__ __forceinline__ void operator()(const uint16_t* seq, int row0, int n, const void* tile) const {
-    const int wave = uniform(threadIdx.x >> 6), first = TR == 64 ? 0 : wave >> 1;
-    const char* base = reinterpret_cast<const char*>(seq) + static_cast<int64_t>(row0) * stride + 64 * first;
-    const uint32_t lds = lds_addr(tile) + 1024 * (TR == 64 ? wave : wave & 1) + TR * 64 * first;
+    const char* base = reinterpret_cast<const char*>(seq) + static_cast<int64_t>(row0) * stride;
+    const uint32_t lds = lds_addr(tile) + 1024 * uniform(threadIdx.x >> 6);
     const uint32_t o = static_cast<uint32_t>(min(row, n - 1 - row0)) * stride + off;
-    constexpr int kStep = TR == 64 ? 1 : 2;
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) dma_b128(o, base + 64 * kStep * i, lds + TR * 64 * kStep * i);
+    for (int i = 0; i < D / 32; ++i) copy16(o, base + 64 * i, lds + kSlice * i);
   }
 };
 
@@ -94,14 +76,12 @@ struct Offs {
 };
 
 // elements 16 ks + 8 h .. +7 of row 32 w + (lane & 31)
-template <int TR>
 __device__ __forceinline__ bf16x8_t read_row(const char* tile, const Offs& o, int w, int ks) {
-  return *reinterpret_cast<const bf16x8_t*>(tile + (ks >> 1) * (TR * 64) + w * 2048 + o.row[ks & 1]);
+  return *reinterpret_cast<const bf16x8_t*>(tile + (ks >> 1) * kSlice + w * 2048 + o.row[ks & 1]);
 }
 // element 32 dt + (lane & 31) of rows 16 m + 4 h .. +3 and 16 m + 8 + 4 h .. +3
-template <int TR>
 __device__ __forceinline__ bf16x8_t read_tr(const char* tile, const Offs& o, int m, int dt) {
-  const char* p = tile + dt * (TR * 64) + m * 1024;
+  const char* p = tile + dt * kSlice + m * 1024;
   const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + o.tr[0]));
   const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + o.tr[1]));
   const u32x2_t x = __builtin_bit_cast(u32x2_t, a), y = __builtin_bit_cast(u32x2_t, b);
@@ -223,7 +203,7 @@ __global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* _
   const int q0 = (at.weight - 1) * kRows, w0 = q0 + 32 * wave, qi = w0 + l32;
   const float c = a.scale * kLog2e;
   const Offs of;
-  const Copier<D, 64> ck(a.k_stride), cv(a.v_stride);
+  const Copier<D> ck(a.k_stride), cv(a.v_stride);
   const uint16_t* kb = a.k + at.first * a.k_stride + hk * D;
   const uint16_t* vb = a.v + at.first * a.v_stride + hk * D;
   const int tiles = (min(at.n, q0 + kRows) + kTile - 1) / kTile;
@@ -247,7 +227,7 @@ __global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* _
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int w = 0; w < 2; ++w) s[w] = mfma(read_row<64>(kt, of, w, ks), qf[ks], s[w]);
+      for (int w = 0; w < 2; ++w) s[w] = mfma(read_row(kt, of, w, ks), qf[ks], s[w]);
   };
   auto maximum = [&](const f32x16_t (&s)[2]) __attribute__((always_inline)) {
     float top = s[0][0];
@@ -279,7 +259,7 @@ __global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* _
       for (int mm = 0; mm < 2; ++mm) {
         const bf16x8_t pf = pack8(s[w], mm);
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) acc[dt] = mfma(read_tr<64>(vt, of, 2 * w + mm, dt), pf, acc[dt]);
+        for (int dt = 0; dt < DT; ++dt) acc[dt] = mfma(read_tr(vt, of, 2 * w + mm, dt), pf, acc[dt]);
       }
     }
   };
@@ -363,7 +343,7 @@ __global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, GradArgs 
   const int q0 = (at.weight - 1) * kRows, w0 = q0 + 32 * wave, qi = w0 + l32;
   const float c = a.scale * kLog2e;
   const Offs of;
-  const Copier<D, 64> ck(a.k_stride), cv(a.v_stride);
+  const Copier<D> ck(a.k_stride), cv(a.v_stride);
   const uint16_t* kb = a.k + at.first * a.k_stride + hk * D;
   const uint16_t* vb = a.v + at.first * a.v_stride + hk * D;
   const int tiles = (min(at.n, q0 + kRows) + kTile - 1) / kTile;
@@ -419,8 +399,8 @@ __global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, GradArgs 
     p.dp = zero16();
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      p.s = mfma(read_row<64>(kt, of, w, ks), qf[ks], p.s);
-      p.dp = mfma(read_row<64>(vt, of, w, ks), gf[ks], p.dp);
+      p.s = mfma(read_row(kt, of, w, ks), qf[ks], p.s);
+      p.dp = mfma(read_row(vt, of, w, ks), gf[ks], p.dp);
     }
   };
   auto apply = [&](int j, int w, Pair& p, auto masked) __attribute__((always_inline)) {
@@ -435,7 +415,7 @@ __global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, GradArgs 
     for (int m = 0; m < 2; ++m) {
       const bf16x8_t pf = pack8(p.s, m);
 #pragma unroll
-      for (int dt = 0; dt < DT; ++dt) acc[dt] = mfma(read_tr<64>(kt, of, 2 * w + m, dt), pf, acc[dt]);
+      for (int dt = 0; dt < DT; ++dt) acc[dt] = mfma(read_tr(kt, of, 2 * w + m, dt), pf, acc[dt]);
     }
   };
   auto step = [&](int j, auto masked) __attribute__((always_inline)) {
@@ -490,7 +470,7 @@ __global__ __launch_bounds__(256, 1) void k_prompt_bwd_kv(PromptArgs a, GradArgs
   const int k0 = ((at.n + kRows - 1) / kRows - at.weight) * kRows, w0 = k0 + 32 * wave, ki = w0 + l32;
   const float c = a.scale * kLog2e;
   const Offs of;
-  const Copier<D, 64> cq(a.q_stride), cg(g.go_stride);
+  const Copier<D> cq(a.q_stride), cg(g.go_stride);
   const int j0 = k0 / kTile;                                    // first query tile that sees these keys
   const int per = (at.n + kTile - 1) / kTile - j0;
   const uint16_t* qb = a.q + at.first * a.q_stride + h0 * D;
@@ -500,7 +480,7 @@ __global__ __launch_bounds__(256, 1) void k_prompt_bwd_kv(PromptArgs a, GradArgs
     cg(gb + i * D, j * kTile, at.n, lds[buf][1]);
     if (wave < 2) {
       const int64_t row = (static_cast<int64_t>(wave) * a.Hq + h0 + i) * a.T + at.first + min(j * kTile + lane, at.n - 1);
-      dma_b32(g.stat + row, lds_addr(stat[buf][wave]));
+      copy4(g.stat + row, lds_addr(stat[buf][wave]));
     }
   };
 
@@ -528,8 +508,8 @@ __global__ __launch_bounds__(256, 1) void k_prompt_bwd_kv(PromptArgs a, GradArgs
     p.dp = zero16();
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      p.s = mfma(read_row<64>(qt, of, w, ks), kf[ks], p.s);
-      p.dp = mfma(read_row<64>(gt, of, w, ks), vf[ks], p.dp);
+      p.s = mfma(read_row(qt, of, w, ks), kf[ks], p.s);
+      p.dp = mfma(read_row(gt, of, w, ks), vf[ks], p.dp);
     }
   };
   auto weigh = [&](int buf, int j, int w, Pair& p, auto masked) __attribute__((always_inline)) {
@@ -560,8 +540,8 @@ __global__ __launch_bounds__(256, 1) void k_prompt_bwd_kv(PromptArgs a, GradArgs
       const bf16x8_t pf = pack8(p.s, m), sf = pack8(p.dp, m);
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
-        av[dt] = mfma(read_tr<64>(gt, of, 2 * w + m, dt), pf, av[dt]);
-        ak[dt] = mfma(read_tr<64>(qt, of, 2 * w + m, dt), sf, ak[dt]);
+        av[dt] = mfma(read_tr(gt, of, 2 * w + m, dt), pf, av[dt]);
+        ak[dt] = mfma(read_tr(qt, of, 2 * w + m, dt), sf, ak[dt]);
       }
     }
   };
