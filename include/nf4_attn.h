@@ -106,9 +106,10 @@ int nf4_kv_attention(const void* q, int64_t q_stride, int64_t T, int32_t Hq,
                      int64_t P, int32_t page, int32_t Hkv, int32_t D, float scale,
                      void* out, int fill_outside, void* ws, size_t ws_bytes, void* stream);
 
-/* Workspace bytes of nf4_kv_attention for these sizes on the current device;
- * SIZE_MAX for sizes it refuses. */
-size_t nf4_kv_attention_workspace(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D);
+/* Workspace bytes of nf4_kv_attention for these sizes on the current device
+ * (0 for page tables of at most 512 tokens); SIZE_MAX for sizes it refuses. */
+size_t nf4_kv_attention_workspace(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                                  int32_t width, int32_t page);
 
 /*
  * nf4_prompt_attention_fwd -- causal attention inside each packed sequence:

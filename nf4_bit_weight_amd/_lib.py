@@ -81,7 +81,7 @@ SIGNATURES = {
                              _vp, _vp, _int, _vp]),
     "nf4_kv_dequantize": (_int, [_i64, *_SEQS, *_CACHE, _vp, _vp, _int, _vp]),
     "nf4_kv_attention": (_int, [_vp, _i64, _i64, _i32, *_SEQS, *_CACHE, _f32, _vp, _int, _vp, _size, _vp]),
-    "nf4_kv_attention_workspace": (_size, [_i64, _i32, _i32, _i32, _i32]),
+    "nf4_kv_attention_workspace": (_size, [_i64, _i32, _i32, _i32, _i32, _i32, _i32]),
     "nf4_prompt_attention_fwd": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i32, _i32, _i32, _i32, _f32,
                                         _vp, _vp, _vp, _int, _vp]),
     "nf4_prompt_attention_bwd": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i32, _i32,

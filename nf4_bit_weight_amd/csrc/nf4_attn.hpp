@@ -51,14 +51,17 @@ hipError_t launch_kv_dequantize(const KVCache& c, const KVSeqs& s, void* k_out, 
                                 hipStream_t stream);
 
 // How a cache attention call is cut: `workers` workgroups share the steps of
-// all (sequence, row tile, key head) units evenly; a unit that several of them
-// share is joined from their partial results by a second kernel.
+// all (sequence, row tile, key head) units evenly, and a unit that several of
+// them share is joined from their partial results by a second kernel; or, in
+// a solo call, each of them takes one unit whole.
 struct KVAttnPlan {
   int mt;          // row tiles of 16 (query row, head) rows per unit
-  int workers;
+  bool solo;
+  int64_t workers;
+  int64_t steps;   // bound on the units times the most steps of one
   size_t ws_bytes;
 };
-KVAttnPlan plan_kv_attention(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int cus);
+KVAttnPlan plan_kv_attention(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int64_t tokens, int cus);
 hipError_t launch_kv_attention(const KVAttnPlan& pl, const KVCache& c, const KVSeqs& s, const void* q,
                                int64_t q_stride, int32_t Hq, float scale, void* out, int fill, void* ws,
                                hipStream_t stream);

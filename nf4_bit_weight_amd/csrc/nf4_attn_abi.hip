@@ -107,10 +107,11 @@ int nf4_kv_dequantize(int64_t T, const int32_t* offsets, const int32_t* lengths,
   return to_status(e);
 }
 
-size_t nf4_kv_attention_workspace(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
-  if (check_heads(T, B, Hq, Hkv, D)) return SIZE_MAX;
+size_t nf4_kv_attention_workspace(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t width,
+                                  int32_t page) {
+  if (check_heads(T, B, Hq, Hkv, D) || width < 0 || page < 1) return SIZE_MAX;
   if (T == 0) return 0;
-  return plan_kv_attention(T, B, Hq, Hkv, D, device_cu_count()).ws_bytes;
+  return plan_kv_attention(T, B, Hq, Hkv, D, static_cast<int64_t>(width) * page, device_cu_count()).ws_bytes;
 }
 
 int nf4_kv_attention(const void* q, int64_t q_stride, int64_t T, int32_t Hq, const int32_t* offsets,
@@ -127,14 +128,12 @@ int nf4_kv_attention(const void* q, int64_t q_stride, int64_t T, int32_t Hq, con
   if (T > 0 && !out) return NF4_ERR_NULL;
   if (!aligned(out, 16)) return NF4_ERR_ALIGN;
   if (T == 0) return NF4_OK;
-  if (P == 0) width = 0;                                     // no pages: no key is seen
-  const KVAttnPlan pl = plan_kv_attention(T, B, Hq, Hkv, D, device_cu_count());
-  // steps of 128 tokens over all units are counted in 32 bits
-  const int64_t tiles = T * (Hq / Hkv) / (16 * pl.mt) + B;
-  const int64_t steps = (static_cast<int64_t>(width) * page + 127) / 128;
-  if (steps > 0 && tiles * Hkv > (INT32_MAX - pl.workers) / steps) return NF4_ERR_UNSUPPORTED;
-  if (!ws || ws_bytes < pl.ws_bytes) return NF4_ERR_WORKSPACE;
-  if (!aligned(ws, 16)) return NF4_ERR_ALIGN;
+  if (P == 0) width = 0;                                     // no pages: no key is seen (and no workspace is needed)
+  const KVAttnPlan pl = plan_kv_attention(T, B, Hq, Hkv, D, static_cast<int64_t>(width) * page, device_cu_count());
+  // units and their steps of 128 tokens are counted in 32 bits
+  if (pl.steps > INT32_MAX / 2 || pl.workers > INT32_MAX / 2) return NF4_ERR_UNSUPPORTED;
+  if (pl.ws_bytes > 0 && (!ws || ws_bytes < pl.ws_bytes)) return NF4_ERR_WORKSPACE;
+  if (pl.ws_bytes > 0 && !aligned(ws, 16)) return NF4_ERR_ALIGN;
   const KVCache c{const_cast<uint8_t*>(k_codes), const_cast<float*>(k_scale), const_cast<uint8_t*>(v_codes),
                   const_cast<float*>(v_scale), P, page, Hkv, D};
   const KVSeqs s{offsets, lengths, page_table, B, width, static_cast<int32_t>(T)};

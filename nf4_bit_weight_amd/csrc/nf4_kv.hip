@@ -31,8 +31,8 @@ __device__ __forceinline__ Place place_of(const KVSeqs& s, const KVCache& c, int
 // ---- append ----------------------------------------------------------------
 // One workgroup takes TT consecutive rows (and, with TT == 1, 256 * 8 elements
 // of them).  The sines and cosines of its rows are computed once in 64 bits into
-// LDS and shared by all heads; a thread then turns 8 neighbouring elements,
-// reading their partners a second time (from cache), and the 8 threads of a
+// LDS; a thread keeps those of its 8 neighbouring elements for all heads, reads
+// the elements' partners a second time (from cache), and the 8 threads of a
 // block of 64 agree on its largest magnitude.  Bound by memory: 2 bytes in per
 // element and 0.5 to 2.5 out.
 template <int D, int TT>
@@ -56,46 +56,63 @@ __global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendAr
     }
   }
   __syncthreads();
-  const int first_k = a.q ? a.Hq : 0, total = (first_k + 2 * c.Hkv) * kPer;
-  for (int i = blockIdx.y * 256 + threadIdx.x; i < total; i += 256 * gridDim.y) {
-    const int hd = i / kPer, r = i % kPer / D8, e = 8 * (i % D8);
-    if (r >= rows) continue;
-    const int64_t t = t0 + r;
+  // a thread keeps its row and elements and goes over the heads
+  const int j = threadIdx.x % kPer, r = j / D8, e = 8 * (j % D8);
+  if (r >= rows) return;
+  const int first_k = a.q ? a.Hq : 0, heads = first_k + 2 * c.Hkv, seq = seqs[r];
+  const int64_t t = t0 + r, base = vecs[r];
+  const bool turned = e < 2 * half, low = e < half;
+  const int pair = a.interleaved ? e / 2 : low ? e : e - half, partner = low ? e + half : e - half;
+  double2 cs[8];
+  if (turned && seq >= 0) {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) cs[p] = turn[r * 64 + min(pair + p, 63)];
+  }
+  constexpr int kHeads = 256 / kPer;
+  auto source = [&](int hd) __attribute__((always_inline)) {
+    return hd < first_k ? a.q + t * a.q_stride + hd * D
+                        : hd < first_k + c.Hkv ? a.k + t * a.k_stride + (hd - first_k) * D
+                                               : a.v + t * a.v_stride + (hd - first_k - c.Hkv) * D;
+  };
+  const int step = kHeads * gridDim.y;
+  int hd = blockIdx.y * kHeads + threadIdx.x / kPer;
+  uint4 next{}, next_o{};
+  auto ask = [&](int i) __attribute__((always_inline)) {
+    if (i >= heads || seq < 0) return;
+    const uint16_t* src = source(i);
+    next = *reinterpret_cast<const uint4*>(src + e);
+    if (turned && !a.interleaved && i < first_k + c.Hkv) next_o = *reinterpret_cast<const uint4*>(src + partner);
+  };
+  ask(hd);
+  for (; hd < heads; hd += step) {
     const bool is_q = hd < first_k, is_v = hd >= first_k + c.Hkv;
     const int h = is_q ? hd : is_v ? hd - first_k - c.Hkv : hd - first_k;
     uint16_t* dst = is_q ? a.q_out + (t * a.Hq + h) * D + e
                          : (!is_v && a.k_out) ? a.k_out + (t * c.Hkv + h) * D + e : nullptr;
-    if (seqs[r] < 0) {
+    if (seq < 0) {
       if (dst && a.fill) *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
       continue;
     }
-    const uint16_t* src = is_q ? a.q + t * a.q_stride + h * D
-                               : is_v ? a.v + t * a.v_stride + h * D : a.k + t * a.k_stride + h * D;
-    uint4 w = *reinterpret_cast<const uint4*>(src + e);
-    uint32_t x[4] = {w.x, w.y, w.z, w.w};
-    if (!is_v && e < 2 * half) {
+    uint32_t x[4] = {next.x, next.y, next.z, next.w};
+    const uint32_t o[4] = {next_o.x, next_o.y, next_o.z, next_o.w};
+    ask(hd + step);
+    if (!is_v && turned) {
       if (a.interleaved) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const double2 cs = turn[r * 64 + e / 2 + p];
           const double u = static_cast<double>(__builtin_bit_cast(float, x[p] << 16));
           const double y = static_cast<double>(__builtin_bit_cast(float, x[p] & 0xFFFF0000u));
-          x[p] = pack_bf16x2(static_cast<float>(u * cs.x - y * cs.y), static_cast<float>(y * cs.x + u * cs.y));
+          x[p] = pack_bf16x2(static_cast<float>(u * cs[p].x - y * cs[p].y), static_cast<float>(y * cs[p].x + u * cs[p].y));
         }
       } else {
-        const bool low = e < half;
-        const uint4 wo = *reinterpret_cast<const uint4*>(src + (low ? e + half : e - half));
-        const uint32_t o[4] = {wo.x, wo.y, wo.z, wo.w};
         const uint32_t flip = low ? 0x80000000u : 0u;           // a c - b s below, b c + a s above
-        const int f = low ? e : e - half;
         float z[8];
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
-          const double2 cs = turn[r * 64 + f + p];
           const uint32_t mi = p & 1 ? x[p / 2] & 0xFFFF0000u : x[p / 2] << 16;
           const uint32_t ot = (p & 1 ? o[p / 2] & 0xFFFF0000u : o[p / 2] << 16) ^ flip;
-          z[p] = static_cast<float>(static_cast<double>(__builtin_bit_cast(float, mi)) * cs.x +
-                                    static_cast<double>(__builtin_bit_cast(float, ot)) * cs.y);
+          z[p] = static_cast<float>(static_cast<double>(__builtin_bit_cast(float, mi)) * cs[p].x +
+                                    static_cast<double>(__builtin_bit_cast(float, ot)) * cs[p].y);
         }
 #pragma unroll
         for (int p = 0; p < 4; ++p) x[p] = pack_bf16x2(z[2 * p], z[2 * p + 1]);
@@ -113,7 +130,6 @@ __global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendAr
     }
 #pragma unroll
     for (int d = 1; d < 8; d *= 2) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
-    const int64_t base = vecs[r];
     if (base < 0) continue;
     const float amax = __builtin_bit_cast(float, top << 16);
     const bool bad = top >= 0x7F80u, dead = amax < kDeadBlock;
@@ -195,6 +211,7 @@ __global__ __launch_bounds__(256) void k_kv_dequantize(KVCache c, KVSeqs s, uint
 // (values), never an element.
 constexpr int kStep = 128;           // tokens per workgroup step, 32 a wave
 constexpr float kSlack = 8.0f;       // see the running maximum below
+constexpr int kSoloSteps = 4;
 
 template <int D, int MT>
 struct KVPart {                       // one worker's partial result of a unit
@@ -206,33 +223,69 @@ struct SeqInfo {
   int first, n, len, tiles, steps;   // tiles of rows; steps per (tile, head)
 };
 
+// All sequences as the kernels count them.  Lane l holds sequence l, the first
+// 64 are read once.  Whole units are dealt out in `solo` calls, steps otherwise.
 template <int MT>
-__device__ __forceinline__ SeqInfo seq_info(const KVSeqs& s, int b, int G, int cap) {
-  SeqInfo i;
-  seq_rows(s.offsets, b, s.T, i.first, i.n);
-  i.len = s.lengths[b];
-  const int seen = min(max(i.len, 0), cap);
-  i.tiles = (i.n * G + 16 * MT - 1) / (16 * MT);
-  i.steps = (seen + kStep - 1) / kStep;
-  return i;
-}
-
-// Steps of the whole call, those of the sequences before `upto`, and the steps
-// each worker takes.
-template <int MT>
-__device__ __forceinline__ void share(const KVSeqs& s, int Hkv, int G, int cap, int workers, int upto, int& total,
-                                      int& before, int& per) {
-  int sum = 0, pre = 0;
-  for (int b = threadIdx.x & 63; b < s.B; b += 64) {
-    const SeqInfo i = seq_info<MT>(s, b, G, cap);
-    const int st = Hkv * i.tiles * i.steps;
-    sum += st;
-    if (b < upto) pre += st;
+struct Seqs {
+  const KVSeqs& s;
+  int Hkv, G, cap;
+  bool solo;
+  SeqInfo mine;
+  __device__ __forceinline__ Seqs(const KVSeqs& s_, int Hkv_, int G_, int cap_, bool solo_)
+      : s(s_), Hkv(Hkv_), G(G_), cap(cap_), solo(solo_) {
+    mine = load(threadIdx.x & 63);
   }
-  total = wave_sum(sum);
-  before = wave_sum(pre);
-  per = max(1, (total + workers - 1) / workers);
-}
+  __device__ __forceinline__ SeqInfo load(int b) const {
+    SeqInfo i{0, 0, 0, 0, 0};
+    if (b < s.B) {
+      seq_rows(s.offsets, b, s.T, i.first, i.n);
+      i.len = s.lengths[b];
+      i.tiles = (i.n * G + 16 * MT - 1) / (16 * MT);
+      i.steps = (min(max(i.len, 0), cap) + kStep - 1) / kStep;
+    }
+    return i;
+  }
+  __device__ __forceinline__ int weight(const SeqInfo& i) const { return Hkv * i.tiles * (solo ? 1 : i.steps); }
+  __device__ __forceinline__ SeqInfo of_lane(int b0) const {    // sequence b0 + lane
+    return b0 == 0 ? mine : load(b0 + (threadIdx.x & 63));
+  }
+  __device__ __forceinline__ SeqInfo get(int b) const {         // the same b in the whole wave
+    if (b < 64) {
+      return SeqInfo{__builtin_amdgcn_readlane(mine.first, b), __builtin_amdgcn_readlane(mine.n, b),
+                     __builtin_amdgcn_readlane(mine.len, b), __builtin_amdgcn_readlane(mine.tiles, b),
+                     __builtin_amdgcn_readlane(mine.steps, b)};
+    }
+    const SeqInfo i = load(b);
+    return SeqInfo{uniform(i.first), uniform(i.n), uniform(i.len), uniform(i.tiles), uniform(i.steps)};
+  }
+  // Weight of all sequences and of those before `upto`.
+  __device__ __forceinline__ void sums(int upto, int& total, int& before) const {
+    int sum = 0, pre = 0;
+    for (int b0 = 0; b0 < s.B; b0 += 64) {
+      const int w = weight(of_lane(b0));
+      sum += w;
+      if (b0 + static_cast<int>(threadIdx.x & 63) < upto) pre += w;
+    }
+    total = wave_sum(sum);
+    before = wave_sum(pre);
+  }
+  // The sequence that holds unit of weight `lo`, and the weight before it.
+  __device__ __forceinline__ void find(int lo, int& b, int& base) const {
+    b = s.B;
+    base = 0;
+    for (int b0 = 0; b0 < s.B; b0 += 64) {
+      const int w = weight(of_lane(b0)), incl = wave_scan(w);
+      const uint64_t hit = __ballot(base + incl > lo);
+      if (hit) {
+        const int l = __builtin_ctzll(hit);
+        b = b0 + l;
+        base += __builtin_amdgcn_readlane(incl - w, l);
+        return;
+      }
+      base += __builtin_amdgcn_readlane(incl, 63);
+    }
+  }
+};
 
 // What one wave reads of 32 tokens, in LDS: the patterns of keys and values as
 // they lie in their pages ([2 tiles][16 tokens][D / 2]) and the scales ([2][16]
@@ -262,7 +315,8 @@ __device__ __forceinline__ bf16x8_t fp4_to_frag(uint32_t c) {
 template <int D, int MT>
 __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_kv_attention(KVCache c, KVSeqs s, const uint16_t* __restrict__ q,
                                                       int64_t q_stride, int Hq, float scale2,
-                                                      uint16_t* __restrict__ out, float* __restrict__ ws) {
+                                                      uint16_t* __restrict__ out, float* __restrict__ ws, bool solo,
+                                                      int fill) {
   constexpr int NB = D / 64, R = 16 * MT, kCopies = KVTile<D>::kCopies;
   // the ring, and between segments the waves' results
   constexpr size_t kRingBytes = 4 * kRing * sizeof(KVTile<D>), kJoinBytes = 2 * (R * D + 2 * R) * sizeof(float);
@@ -271,47 +325,36 @@ __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_kv_attention(KVCache c
   const int G = Hq / c.Hkv, cap = s.width * c.page;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  int total, none, per;
-  share<MT>(s, c.Hkv, G, cap, gridDim.x, 0, total, none, per);
+  const Seqs<MT> seqs(s, c.Hkv, G, cap, solo);
+  int total, none;
+  seqs.sums(0, total, none);
+  const int per = solo ? 1 : max(1, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
   int lo = min(static_cast<int64_t>(total), static_cast<int64_t>(blockIdx.x) * per);
   const int hi = min(total, lo + per);
+  if (solo && fill && s.offsets) {                 // rows outside every sequence: with a join, it writes them
+    const int from = min(max(s.offsets[0], 0), s.T), to = min(max(s.offsets[s.B], from), s.T);
+    for (int i = blockIdx.x; i < from + s.T - to; i += gridDim.x) {
+      uint32_t* row = reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(i < from ? i : to + (i - from)) * Hq * D);
+      for (int e = threadIdx.x; e < Hq * D / 2; e += 256) row[e] = 0u;
+    }
+  }
   if (lo >= hi) return;
   const int begin = lo;
 
-  // the sequence whose steps hold `lo`, and the steps before it
-  int b = 0, base = 0;
-  for (int b0 = 0; b0 < s.B; b0 += 64) {
-    const int bb = b0 + lane;
-    int st = 0;
-    if (bb < s.B) {
-      const SeqInfo i = seq_info<MT>(s, bb, G, cap);
-      st = c.Hkv * i.tiles * i.steps;
-    }
-    const int incl = wave_scan(st);
-    const uint64_t hit = __ballot(base + incl > lo);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      b = b0 + l;
-      base += __shfl(incl - st, l);
-      break;
-    }
-    base += __shfl(incl, 63);
-  }
-  b = uniform(b);
-  base = uniform(base);
-
+  int b, base;
+  seqs.find(lo, b, base);
   const uint32_t sel = r16 >= 8 ? 0x07030602u : 0x05010400u;
 
   while (lo < hi && b < s.B) {
-    const SeqInfo si = seq_info<MT>(s, b, G, cap);
-    const int n = uniform(si.n), len = uniform(si.len), ns = uniform(si.steps), first = uniform(si.first);
-    const int units = c.Hkv * uniform(si.tiles);
-    if (lo >= base + units * ns) {                 // nothing (left) of this sequence
-      base += units * ns;
+    const SeqInfo si = seqs.get(b);
+    const int n = si.n, len = si.len, first = si.first, weight = seqs.weight(si);
+    if (lo >= base + weight) {                     // nothing (left) of this sequence
+      base += weight;
       ++b;
       continue;
     }
-    const int u = (lo - base) / ns, s0 = lo - base - u * ns, s1 = min(ns, s0 + (hi - lo));
+    const int ns = si.steps, share = solo ? 1 : ns;
+    const int u = (lo - base) / share, s0 = lo - base - u * share, s1 = solo ? ns : min(ns, s0 + (hi - lo));
     const int rt = u / c.Hkv, h = u - rt * c.Hkv;
     // read by the scalar unit: nothing writes the table while the kernel runs
     typedef const __attribute__((address_space(4))) int32_t table_t;
@@ -644,7 +687,7 @@ __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_kv_attention(KVCache c
         }
       }
     }
-    lo += s1 - s0;
+    lo += solo ? 1 : s1 - s0;
     __syncthreads();                                               // the results are read before the ring is filled again
   }
 }
@@ -664,9 +707,11 @@ __global__ __launch_bounds__(256) void k_kv_join(KVCache c, KVSeqs s, int Hq, ui
     if (fill && threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(dst)[threadIdx.x] = 0u;
     return;
   }
-  int total, before, per;
-  share<MT>(s, c.Hkv, G, cap, workers, bb, total, before, per);
-  const SeqInfo si = seq_info<MT>(s, bb, G, cap);
+  const Seqs<MT> seqs(s, c.Hkv, G, cap, false);
+  int total, before;
+  seqs.sums(bb, total, before);
+  const int per = max(1, (total + workers - 1) / workers);
+  const SeqInfo si = seqs.get(bb);
   if (si.steps == 0) {
     if (threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(dst)[threadIdx.x] = 0u;
     return;
@@ -678,7 +723,7 @@ __global__ __launch_bounds__(256) void k_kv_join(KVCache c, KVSeqs s, int Hq, ui
   const int grp = threadIdx.x / LP, e = 4 * (threadIdx.x % LP);
   float m = -INFINITY, l = 0.0f;
   f32x4_t a = {0.f, 0.f, 0.f, 0.f};
-  constexpr int kAhead = 4;                                  // partial results asked for at once
+  constexpr int kAhead = 8;                                  // partial results asked for at once
   for (int w = w0 + grp; w <= w1; w += kAhead * NG) {
     float om[kAhead], os[kAhead];
     f32x4_t o[kAhead];
@@ -729,12 +774,13 @@ hipError_t attend(const KVAttnPlan& pl, const KVCache& c, const KVSeqs& s, const
                   float scale, void* out, int fill, void* ws, hipStream_t stream) {
   // scores in units of log2: exp(x) = exp2(x log2 e)
   const float scale2 = scale * 1.44269504088896340736f;
-  k_kv_attention<D, MT><<<pl.workers, 256, 0, stream>>>(c, s, static_cast<const uint16_t*>(q), q_stride, Hq, scale2,
-                                                        static_cast<uint16_t*>(out), static_cast<float*>(ws));
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  k_kv_attention<D, MT><<<static_cast<unsigned>(pl.workers), 256, 0, stream>>>(
+      c, s, static_cast<const uint16_t*>(q), q_stride, Hq, scale2, static_cast<uint16_t*>(out), static_cast<float*>(ws),
+      pl.solo, fill);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || pl.solo) return e;
   k_kv_join<D, MT><<<dim3(s.T, Hq), 256, 0, stream>>>(c, s, Hq, static_cast<uint16_t*>(out),
-                                                      static_cast<const float*>(ws), pl.workers, fill);
+                                                      static_cast<const float*>(ws), static_cast<int>(pl.workers), fill);
   return hipGetLastError();
 }
 
@@ -779,13 +825,16 @@ hipError_t launch_kv_dequantize(const KVCache& c, const KVSeqs& s, void* k_out, 
   return hipGetLastError();
 }
 
-KVAttnPlan plan_kv_attention(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int cus) {
+KVAttnPlan plan_kv_attention(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int64_t tokens, int cus) {
   KVAttnPlan pl;
   const int64_t G = Hq / Hkv;
   const int64_t mean = B > 0 ? (T * G + B - 1) / B : G;      // rows per sequence and key head
   pl.mt = mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
-  pl.workers = 2 * cus;
-  pl.ws_bytes = 2 * static_cast<size_t>(pl.workers) * (16 * pl.mt * (D + 2)) * sizeof(float);
+  const int64_t units = (T * G / (16 * pl.mt) + B) * Hkv, steps = (tokens + kStep - 1) / kStep;
+  pl.solo = steps <= kSoloSteps;
+  pl.workers = pl.solo ? units : 2 * cus;
+  pl.steps = steps > 0 && units > INT64_MAX / steps ? INT64_MAX : units * (steps > 0 ? steps : 1);
+  pl.ws_bytes = pl.solo ? 0 : 2 * static_cast<size_t>(pl.workers) * (16 * pl.mt * (D + 2)) * sizeof(float);
   return pl;
 }
 

@@ -565,6 +565,7 @@ __global__ __launch_bounds__(256, 1) void k_prompt_bwd_kv(PromptArgs a, GradArgs
       }
       land();
       if (st + 1 < steps) copy_step(buf ^ 1, i, tile_of(k));
+      // one half's weights are computed under the other half's products
       Pair p0, p1;
       scores(buf, 0, p0);
       scores(buf, 1, p1);

@@ -91,15 +91,16 @@ def test_attention_refuses(lib):
     assert attention(lib, out=None) == L.NF4_ERR_NULL
     assert attention(lib, out=BAD) == L.NF4_ERR_ALIGN
     assert attention(lib, T=0, q=None, out=None, ws=None) == L.NF4_OK
-    need = lib.nf4_kv_attention_workspace(2, 1, 4, 2, 64)
+    need = lib.nf4_kv_attention_workspace(2, 1, 4, 2, 64, 100, 16)
     assert 0 < need < BIG
-    assert attention(lib, wsb=need - 1) == L.NF4_ERR_WORKSPACE
-    assert attention(lib, ws=None, wsb=need) == L.NF4_ERR_WORKSPACE
-    assert attention(lib, ws=BAD, wsb=need) == L.NF4_ERR_ALIGN
+    assert attention(lib, width=100, wsb=need - 1) == L.NF4_ERR_WORKSPACE
+    assert attention(lib, width=100, ws=None, wsb=need) == L.NF4_ERR_WORKSPACE
+    assert attention(lib, width=100, ws=BAD, wsb=need) == L.NF4_ERR_ALIGN
+    assert lib.nf4_kv_attention_workspace(2, 1, 4, 2, 64, 32, 16) == 0       # at most 512 tokens: nothing to join
     # more 128-token steps over all units than 32 bits count
     assert attention(lib, T=1 << 26, B=1 << 26, off=None, Hq=32, Hkv=32, D=64, width=1 << 16, page=256, P=1) == L.NF4_ERR_UNSUPPORTED
-    assert lib.nf4_kv_attention_workspace(2, 1, 4, 3, 64) == BIG
-    assert lib.nf4_kv_attention_workspace(0, 0, 4, 2, 64) == 0
+    assert lib.nf4_kv_attention_workspace(2, 1, 4, 3, 64, 1, 16) == BIG
+    assert lib.nf4_kv_attention_workspace(0, 0, 4, 2, 64, 1, 16) == 0
 
 
 def test_dequantize_refuses(lib):

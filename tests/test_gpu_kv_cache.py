@@ -209,7 +209,7 @@ def check_attention(lens, new, Hq, Hkv, D, page, seed=0, width=None, scale=None,
     want, bound, at = torch.zeros(T, Hq, D, dtype=torch.float64), torch.zeros(T, Hq, D, dtype=torch.float64), 0
     for b, (ln, m) in enumerate(zip(lens, n)):
         k, v = h.dense(b, ln)
-        pos = torch.arange(ln - m, ln)
+        pos = torch.arange(ln - m, ln)          # (rows before the first token see nothing)
         seen = torch.arange(ln)[None] <= pos[:, None]
         r = slice(at, at + m)
         want[r], bound[r] = R.attend(q[r].double(), k, v, seen, float(np.float32(sc)))
@@ -227,6 +227,12 @@ def test_attention_heads(D, Hq, Hkv):
 @pytest.mark.parametrize("n", [1, 15, 16, 17, 31, 32, 33, 127, 128, 129, 255, 257, 1000])
 def test_attention_lengths(n):
     check_attention([n], None, 4, 2, 128, 48, seed=n)
+
+
+@pytest.mark.parametrize("n", [1, 16, 129, 512, 513])
+def test_attention_wide_tables(n):
+    """Short sequences in a table for long ones, where workgroups share units."""
+    check_attention([n, 0, 3], None, 4, 2, 64, 16, seed=n, width=200)
 
 
 @pytest.mark.parametrize("page", [16, 32, 48, 80, 256])
@@ -360,7 +366,7 @@ def test_repeatable_streams_and_workspaces():
     q = R.normal(2, 3, 8, 64).to(DEV)
     ln = i32(lens)
     ref = nf4_kv_attention(q, cache, ln, table)
-    need = nf4_kv_attention_workspace(3, 3, 8, 2, 64)
+    need = nf4_kv_attention_workspace(3, 3, 8, 2, 64, *table.shape[1:], 32)
     ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
     assert torch.equal(nf4_kv_attention(q, cache, ln, table, ws=ws), ref)
     with pytest.raises(RuntimeError):
