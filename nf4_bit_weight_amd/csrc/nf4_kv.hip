@@ -31,9 +31,9 @@ __device__ __forceinline__ Place place_of(const KVSeqs& s, const KVCache& c, int
 // ---- append ----------------------------------------------------------------
 // One workgroup takes TT consecutive rows (and, with TT == 1, 256 * 8 elements
 // of them).  The sines and cosines of its rows are computed once in 64 bits into
-// LDS; a thread keeps those of its 8 neighbouring elements for all heads, reads
-// the elements' partners a second time (from cache), and the 8 threads of a
-// block of 64 agree on its largest magnitude.  Bound by memory: 2 bytes in per
+// LDS; a thread keeps those of its 8 neighbouring elements for all heads, takes
+// the elements' partners from another lane, and the 8 threads of a block of 64
+// agree on its largest magnitude.  Bound by memory: 2 bytes in per
 // element and 0.5 to 2.5 out.
 template <int D, int TT>
 __global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendArgs a) {
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendAr
   const int first_k = a.q ? a.Hq : 0, heads = first_k + 2 * c.Hkv, seq = seqs[r];
   const int64_t t = t0 + r, base = vecs[r];
   const bool turned = e < 2 * half, low = e < half;
-  const int pair = a.interleaved ? e / 2 : low ? e : e - half, partner = low ? e + half : e - half;
+  const int pair = a.interleaved ? e / 2 : low ? e : e - half;
   double2 cs[8];
   if (turned && seq >= 0) {
 #pragma unroll
@@ -74,28 +74,30 @@ __global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendAr
                         : hd < first_k + c.Hkv ? a.k + t * a.k_stride + (hd - first_k) * D
                                                : a.v + t * a.v_stride + (hd - first_k - c.Hkv) * D;
   };
-  const int step = kHeads * gridDim.y;
-  int hd = blockIdx.y * kHeads + threadIdx.x / kPer;
-  uint4 next{}, next_o{};
-  auto ask = [&](int i) __attribute__((always_inline)) {
-    if (i >= heads || seq < 0) return;
-    const uint16_t* src = source(i);
-    next = *reinterpret_cast<const uint4*>(src + e);
-    if (turned && !a.interleaved && i < first_k + c.Hkv) next_o = *reinterpret_cast<const uint4*>(src + partner);
+  // kAhead heads are on their way while one is worked on
+  constexpr int kAhead = 3;
+  const int step = kHeads * gridDim.y, lane = threadIdx.x & 63, partner_lane = lane + (low ? half : -half) / 8;
+  const int hd0 = blockIdx.y * kHeads + threadIdx.x / kPer;
+  uint4 ring[kAhead];
+  auto ask = [&](int i, uint4& to) __attribute__((always_inline)) {
+    if (i < heads && seq >= 0) to = *reinterpret_cast<const uint4*>(source(i) + e);
   };
-  ask(hd);
-  for (; hd < heads; hd += step) {
+  auto work = [&](int hd, uint4& slot) __attribute__((always_inline)) {
     const bool is_q = hd < first_k, is_v = hd >= first_k + c.Hkv;
     const int h = is_q ? hd : is_v ? hd - first_k - c.Hkv : hd - first_k;
     uint16_t* dst = is_q ? a.q_out + (t * a.Hq + h) * D + e
                          : (!is_v && a.k_out) ? a.k_out + (t * c.Hkv + h) * D + e : nullptr;
     if (seq < 0) {
       if (dst && a.fill) *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
-      continue;
+      return;
     }
-    uint32_t x[4] = {next.x, next.y, next.z, next.w};
-    const uint32_t o[4] = {next_o.x, next_o.y, next_o.z, next_o.w};
-    ask(hd + step);
+    uint32_t x[4] = {slot.x, slot.y, slot.z, slot.w};
+    ask(hd + kAhead * step, slot);
+    uint32_t o[4];
+    if (!a.interleaved && half) {                               // the partners' elements lie in other lanes of the row
+#pragma unroll
+      for (int p = 0; p < 4; ++p) o[p] = __shfl(static_cast<int>(x[p]), partner_lane);
+    }
     if (!is_v && turned) {
       if (a.interleaved) {
 #pragma unroll
@@ -119,7 +121,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendAr
       }
     }
     if (dst) *reinterpret_cast<uint4*>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
-    if (is_q) continue;
+    if (is_q) return;
     // the largest magnitude of the block, as bit patterns: they order like the
     // values, and a NaN or infinity (0x7F80 and up) comes out on top
     uint32_t top = 0;
@@ -130,7 +132,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendAr
     }
 #pragma unroll
     for (int d = 1; d < 8; d *= 2) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
-    if (base < 0) continue;
+    if (base < 0) return;
     const float amax = __builtin_bit_cast(float, top << 16);
     const bool bad = top >= 0x7F80u, dead = amax < kDeadBlock;
     const float sc = bad ? __builtin_bit_cast(float, 0x7FC00000u) : dead ? 0.0f : amax / 6.0f;
@@ -156,6 +158,13 @@ __global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendAr
     const int64_t vec = base + h * c.page;
     *reinterpret_cast<uint32_t*>((is_v ? c.v_codes : c.k_codes) + vec * (D / 2) + e / 2) = code;
     if ((e & 63) == 0) (is_v ? c.v_scale : c.k_scale)[vec * (D / 64) + e / 64] = sc;
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) ask(hd0 + k * step, ring[k]);
+  for (int hd = hd0; hd < heads; hd += kAhead * step) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (hd + k * step < heads) work(hd + k * step, ring[k]);
   }
 }
 
@@ -786,10 +795,11 @@ hipError_t attend(const KVAttnPlan& pl, const KVCache& c, const KVSeqs& s, const
 
 }  // namespace
 
-// Rows per workgroup: 16, so that the scales of neighbouring tokens share a
-// cache line in one workgroup's writes, where that still makes a workgroup per
-// compute unit; 1, spread over several workgroups, where there are few rows.
-int rows_per_group(int64_t T) { return T >= 4096 ? 16 : T >= 1024 ? 4 : 1; }
+// Rows per workgroup: 4 share a cache line of scales and one start-up; fewer
+// rows than would fill the machine are spread one by one over several
+// workgroups.  17616 rows, 32 heads on 8: 102 us with 4, 106 with 8, 123 with 16
+// (whose 1101 workgroups end in a nearly empty second round).
+int rows_per_group(int64_t T) { return T >= 1024 ? 4 : 1; }
 
 hipError_t launch_kv_append(const KVCache& c, const KVSeqs& s, const AppendArgs& a, hipStream_t stream) {
   const int tt = rows_per_group(s.T);
@@ -799,10 +809,8 @@ hipError_t launch_kv_append(const KVCache& c, const KVSeqs& s, const AppendArgs&
   if (c.D == D_ && tt == TT_) k_kv_append<D_, TT_><<<grid, 256, 0, stream>>>(c, s, a)
   NF4_APPEND(64, 1);
   NF4_APPEND(64, 4);
-  NF4_APPEND(64, 16);
   NF4_APPEND(128, 1);
   NF4_APPEND(128, 4);
-  NF4_APPEND(128, 16);
 #undef NF4_APPEND
   return hipGetLastError();
 }
@@ -817,10 +825,8 @@ hipError_t launch_kv_dequantize(const KVCache& c, const KVSeqs& s, void* k_out, 
   if (c.D == D_ && tt == TT_) k_kv_dequantize<D_, TT_><<<grid, 256, 0, stream>>>(c, s, k, v, fill)
   NF4_DEQUANTIZE(64, 1);
   NF4_DEQUANTIZE(64, 4);
-  NF4_DEQUANTIZE(64, 16);
   NF4_DEQUANTIZE(128, 1);
   NF4_DEQUANTIZE(128, 4);
-  NF4_DEQUANTIZE(128, 16);
 #undef NF4_DEQUANTIZE
   return hipGetLastError();
 }
