@@ -1,4 +1,5 @@
-"""Build libnf4.so in-tree with hipcc for gfx950.
+"""Build libnf4.so in-tree with hipcc for gfx950, and the compiled part of its
+Python binding (_nf4_torch, host code against torch's headers).
 
 Run as `python -m nf4_bit_weight_amd.build` or through __graft_entry__.build().
 Each .hip file compiles to an object in parallel; the objects link into
@@ -36,6 +37,28 @@ HIPCC_FLAGS = [
 ]
 
 
+TORCH_SOURCE = "nf4_torch.cpp"
+TORCH_LIB = os.path.join(PKG, "_nf4_torch.so")
+
+
+def torch_module_cmds(obj: str):
+    """(compile, link) of the binding module: plain host C++."""
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(os.path.abspath(torch.__file__))
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    inc = [os.path.join(base, "include"), sysconfig.get_paths()["include"], os.path.join(rocm, "include")]
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                *[f for d in inc for f in ("-isystem", d)], "-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj]
+    lib = os.path.join(base, "lib")
+    link = ["g++", "-shared", "-fPIC", obj, "-L", PKG, "-l:libnf4.so", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_hip", "-Wl,-rpath,$ORIGIN", "-o", TORCH_LIB + ".tmp"]
+    return compile_, link
+
+
 def hipcc() -> str:
     for cand in (os.environ.get("HIPCC"), "/opt/rocm/bin/hipcc", shutil.which("hipcc")):
         if cand and os.path.exists(cand):
@@ -58,6 +81,9 @@ def build(verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    torch_obj = os.path.join(BUILD_DIR, TORCH_SOURCE.replace(".cpp", ".o"))
+    torch_compile, torch_link = torch_module_cmds(torch_obj)
+    procs.append((TORCH_SOURCE, subprocess.Popen(torch_compile, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -70,7 +96,7 @@ def build(verbose: bool = False) -> str:
         elif verbose and lines:
             print("\n".join(lines))
     if failed:
-        raise RuntimeError(f"hipcc failed for {failed}")
+        raise RuntimeError(f"compilation failed for {failed}")
     tmp = LIB + ".tmp"
     link = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
@@ -78,6 +104,11 @@ def build(verbose: bool = False) -> str:
         print(r.stdout.decode(errors="replace"), file=sys.stderr)
         raise RuntimeError("link of libnf4.so failed")
     os.replace(tmp, LIB)
+    r = subprocess.run(torch_link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        print(r.stdout.decode(errors="replace"), file=sys.stderr)
+        raise RuntimeError("link of _nf4_torch.so failed")
+    os.replace(TORCH_LIB + ".tmp", TORCH_LIB)
     return LIB
 
 
