@@ -221,6 +221,8 @@ __global__ __launch_bounds__(256) void k_kv_dequantize(KVCache c, KVSeqs s, uint
 constexpr int kStep = 128;           // tokens per workgroup step, 32 a wave
 constexpr float kSlack = 8.0f;       // see the running maximum below
 constexpr int kSoloSteps = 4;
+constexpr int kWorkers = 2;
+constexpr int64_t kWideRows = 1024;
 
 template <int D, int MT>
 struct KVPart {                       // one worker's partial result of a unit
@@ -328,7 +330,7 @@ __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_kv_attention(KVCache c
                                                       int fill) {
   constexpr int NB = D / 64, R = 16 * MT, kCopies = KVTile<D>::kCopies;
   // the ring, and between segments the waves' results
-  constexpr size_t kRingBytes = 4 * kRing * sizeof(KVTile<D>), kJoinBytes = 2 * (R * D + 2 * R) * sizeof(float);
+  constexpr size_t kRingBytes = 4 * kRing * sizeof(KVTile<D>), kJoinBytes = 4 * (R * D + 2 * R) * sizeof(float);
   __shared__ __align__(1024) char shared[kRingBytes > kJoinBytes ? kRingBytes : kJoinBytes];
   float* const lds = reinterpret_cast<float*>(shared);
   const int G = Hq / c.Hkv, cap = s.width * c.page;
@@ -606,93 +608,59 @@ __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_kv_attention(KVCache c
       if (ok) step_of(st, slot, ok);
     }
 
-    // join the four waves through LDS, two at a time
-    // a row's 4 accumulators of one group are 4 neighbouring elements:
-    // 64 nb + 8 ((4g + i) & 7) + 4 (g >> 1)
-    float* const half_acc = lds;                                   // [2][R][D]
-    float* const half_ms = lds + 2 * R * D;                        // [2][2][R]
+    // Join the four waves through LDS: all write, then every thread adds the
+    // four values of its elements.  A row's 4 accumulators of one group are 4
+    // neighbouring elements, 64 nb + 8 ((4g + i) & 7) + 4 (g >> 1); rows turn
+    // their 16-byte chunks against each other's banks.
+    __syncthreads();                                               // the ring is read to its end
+    float* const ms = lds + 4 * R * D;                             // [wave][maximum, sum][R]
 #pragma unroll
-    for (int m = 0; m < MT; ++m) sum[m] = quad_sum(sum[m]);
-    for (int round = 0; round < 2; ++round) {                      // (the ring is read to its end)
-      const int senders = round == 0 ? 2 : 1;                      // waves 2, 3 -> 0, 1; then 1 -> 0
-      __syncthreads();
-      if (wave >= senders && wave < 2 * senders) {
-        const int at = wave - senders;
+    for (int m = 0; m < MT; ++m) {
+      const int row = 16 * m + r16;
+      const float total_m = quad_sum(sum[m]);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int row = 16 * m + r16;
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int e = 64 * nb + 8 * ((4 * g + i) & 7) + 4 * (g >> 1);
-              *reinterpret_cast<f32x4_t*>(half_acc + (at * R + row) * D + (e ^ (4 * (r16 & 7)))) =
-                  f32x4_t{acc[m][nb][0][i], acc[m][nb][1][i], acc[m][nb][2][i], acc[m][nb][3][i]};
-            }
-          if (g == 0) {
-            half_ms[(2 * at) * R + row] = mx[m];
-            half_ms[(2 * at + 1) * R + row] = sum[m];
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int e = 64 * nb + 8 * ((4 * g + i) & 7) + 4 * (g >> 1);
+          *reinterpret_cast<f32x4_t*>(lds + (wave * R + row) * D + (e ^ (4 * (r16 & 7)))) =
+              f32x4_t{acc[m][nb][0][i], acc[m][nb][1][i], acc[m][nb][2][i], acc[m][nb][3][i]};
         }
-      }
-      __syncthreads();
-      if (wave < senders) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int row = 16 * m + r16;
-          const float om = half_ms[(2 * wave) * R + row], os = half_ms[(2 * wave + 1) * R + row];
-          const float top = fmaxf(mx[m], om), ref = top == -INFINITY ? 0.0f : top;
-          const float fa = __builtin_amdgcn_exp2f(mx[m] - ref), fb = __builtin_amdgcn_exp2f(om - ref);
-          mx[m] = top;
-          sum[m] = sum[m] * fa + os * fb;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int e = 64 * nb + 8 * ((4 * g + i) & 7) + 4 * (g >> 1);
-              const f32x4_t o = *reinterpret_cast<const f32x4_t*>(half_acc + (wave * R + row) * D + (e ^ (4 * (r16 & 7))));
-#pragma unroll
-              for (int x = 0; x < 4; ++x) acc[m][nb][x][i] = acc[m][nb][x][i] * fa + o[x] * fb;
-            }
-        }
+      if (g == 0) {
+        ms[(2 * wave) * R + row] = mx[m];
+        ms[(2 * wave + 1) * R + row] = total_m;
       }
     }
-    if (wave == 0) {
-      const bool complete = s0 == 0 && s1 == ns;
+    __syncthreads();
+    const bool complete = s0 == 0 && s1 == ns;
+    float* const part = ws + (2 * static_cast<size_t>(blockIdx.x) + (lo == begin ? 0 : 1)) * KVPart<D, MT>::kFloats;
+#pragma unroll
+    for (int k = 0; k < R * D / 1024; ++k) {
+      const int idx = k * 256 + threadIdx.x, row = idx / (D / 4), e = 4 * (idx % (D / 4));
+      const int all = rt * R + row, j = all / G;
+      if (all >= n * G) break;                                     // (rows only grow with k)
+      float top = ms[row], f[4], l = 0.0f;
+#pragma unroll
+      for (int w = 1; w < 4; ++w) top = fmaxf(top, ms[(2 * w) * R + row]);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        f[w] = __builtin_amdgcn_exp2f(ms[(2 * w) * R + row] - ref);
+        l = __builtin_fmaf(f[w], ms[(2 * w + 1) * R + row], l);
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(lds + (w * R + row) * D + (e ^ (4 * (row & 7))));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(f[w], x[i], o[i]);
+      }
       if (complete) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int row = rt * R + 16 * m + r16, j = row / G;
-          if (row >= n * G) continue;
-          const float f = sum[m] == 0.0f ? 0.0f : 1.0f / sum[m];
-          uint16_t* dst = out + ((static_cast<int64_t>(first) + j) * Hq + h * G + (row - j * G)) * D;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int e = 64 * nb + 8 * ((4 * g + i) & 7) + 4 * (g >> 1);
-              *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack_bf16x2(acc[m][nb][0][i] * f, acc[m][nb][1][i] * f),
-                                                              pack_bf16x2(acc[m][nb][2][i] * f, acc[m][nb][3][i] * f));
-            }
-        }
+        const float y = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t* dst = out + ((static_cast<int64_t>(first) + j) * Hq + h * G + (all - j * G)) * D + e;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0] * y, o[1] * y), pack_bf16x2(o[2] * y, o[3] * y));
       } else {
-        float* part = ws + (2 * static_cast<size_t>(blockIdx.x) + (lo == begin ? 0 : 1)) * KVPart<D, MT>::kFloats;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int row = 16 * m + r16;
-          if (rt * R + row >= n * G) continue;
-          if (g == 0) {
-            part[R * D + row] = mx[m];
-            part[R * D + R + row] = sum[m];
-          }
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int e = 64 * nb + 8 * ((4 * g + i) & 7) + 4 * (g >> 1);
-              *reinterpret_cast<f32x4_t*>(part + row * D + e) =
-                  f32x4_t{acc[m][nb][0][i], acc[m][nb][1][i], acc[m][nb][2][i], acc[m][nb][3][i]};
-            }
+        *reinterpret_cast<f32x4_t*>(part + row * D + e) = o;
+        if (e == 0) {
+          part[R * D + row] = top;
+          part[R * D + R + row] = l;
         }
       }
     }
@@ -703,17 +671,35 @@ __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_kv_attention(KVCache c
 
 // Joins the partial results of a unit that several workers shared, in the
 // workers' order; rows that see no key and rows outside every sequence are
-// written here too.  One workgroup per (row, query head).
-template <int D, int MT>
+// written here too.  A (row, query head) takes a workgroup where there are few
+// of them (with many partial results each), a wave where there are many.
+struct Partial {
+  float m, l;
+  f32x4_t a;
+  __device__ __forceinline__ void add(float om, float os, const f32x4_t& o) {
+    const float top = fmaxf(m, om), ref = top == -INFINITY ? 0.0f : top;
+    const float fa = __builtin_amdgcn_exp2f(m - ref), fb = __builtin_amdgcn_exp2f(om - ref);
+    m = top;
+    l = l * fa + os * fb;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) a[x] = a[x] * fa + o[x] * fb;
+  }
+};
+
+template <int D, int MT, bool WIDE>
 __global__ __launch_bounds__(256) void k_kv_join(KVCache c, KVSeqs s, int Hq, uint16_t* __restrict__ out,
                                                  const float* __restrict__ ws, int workers, int fill) {
-  constexpr int R = 16 * MT, LP = D / 4, NG = 256 / LP;     // lanes per row, groups of workers
-  __shared__ float red[NG][D + 4];
-  const int G = Hq / c.Hkv, cap = s.width * c.page, t = blockIdx.x, hq = blockIdx.y;
-  uint16_t* dst = out + (static_cast<int64_t>(t) * Hq + hq) * D;
+  constexpr int R = 16 * MT, LP = D / 4, NG = (WIDE ? 256 : 64) / LP;   // lanes per row, groups of workers
+  __shared__ float red[WIDE ? NG : 1][D + 4];
+  const int G = Hq / c.Hkv, cap = s.width * c.page;
+  const int tid = WIDE ? threadIdx.x : threadIdx.x & 63;
+  const int64_t item = WIDE ? static_cast<int64_t>(blockIdx.x) : 4 * static_cast<int64_t>(blockIdx.x) + uniform(threadIdx.x >> 6);
+  if (item >= static_cast<int64_t>(s.T) * Hq) return;
+  const int t = static_cast<int>(item / Hq), hq = static_cast<int>(item - static_cast<int64_t>(t) * Hq);
+  uint16_t* dst = out + item * D;
   const int bb = uniform(seq_of(s.offsets, s.B, s.T, t));
   if (bb < 0) {
-    if (fill && threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(dst)[threadIdx.x] = 0u;
+    if (fill && tid < LP) *reinterpret_cast<uint2*>(dst + 4 * tid) = make_uint2(0u, 0u);
     return;
   }
   const Seqs<MT> seqs(s, c.Hkv, G, cap, false);
@@ -722,60 +708,58 @@ __global__ __launch_bounds__(256) void k_kv_join(KVCache c, KVSeqs s, int Hq, ui
   const int per = max(1, (total + workers - 1) / workers);
   const SeqInfo si = seqs.get(bb);
   if (si.steps == 0) {
-    if (threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(dst)[threadIdx.x] = 0u;
+    if (tid < LP) *reinterpret_cast<uint2*>(dst + 4 * tid) = make_uint2(0u, 0u);
     return;
   }
   const int h = hq / G, row = (t - si.first) * G + (hq - h * G), rt = row / R, rr = row - rt * R;
   const int u0 = before + (rt * c.Hkv + h) * si.steps;
   const int w0 = u0 / per, w1 = (u0 + si.steps - 1) / per;
   if (w0 == w1) return;                                      // one worker wrote the result
-  const int grp = threadIdx.x / LP, e = 4 * (threadIdx.x % LP);
-  float m = -INFINITY, l = 0.0f;
-  f32x4_t a = {0.f, 0.f, 0.f, 0.f};
+  const int grp = tid / LP, e = 4 * (tid % LP);
+  Partial p{-INFINITY, 0.0f, {0.f, 0.f, 0.f, 0.f}};
   constexpr int kAhead = 8;                                  // partial results asked for at once
   for (int w = w0 + grp; w <= w1; w += kAhead * NG) {
     float om[kAhead], os[kAhead];
     f32x4_t o[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int wk = w + k * NG, wr = min(wk, w1);           // the last one again behind the end, unused
+      const int wr = min(w + k * NG, w1);                    // the last one again behind the end, unused
       const float* part = ws + (2 * static_cast<size_t>(wr) + (wr * per >= u0 ? 0 : 1)) * KVPart<D, MT>::kFloats;
       om[k] = part[R * D + rr];
       os[k] = part[R * D + R + rr];
       o[k] = *reinterpret_cast<const f32x4_t*>(part + rr * D + e);
     }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (w + k * NG > w1) break;
-      const float top = fmaxf(m, om[k]), ref = top == -INFINITY ? 0.0f : top;
-      const float fa = __builtin_amdgcn_exp2f(m - ref), fb = __builtin_amdgcn_exp2f(om[k] - ref);
-      m = top;
-      l = l * fa + os[k] * fb;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) a[x] = a[x] * fa + o[k][x] * fb;
+    for (int k = 0; k < kAhead; ++k)
+      if (w + k * NG <= w1) p.add(om[k], os[k], o[k]);
+  }
+  if constexpr (WIDE) {
+    *reinterpret_cast<f32x4_t*>(&red[grp][e]) = p.a;
+    if (e == 0) {
+      red[grp][D] = p.m;
+      red[grp][D + 1] = p.l;
     }
-  }
-  *reinterpret_cast<f32x4_t*>(&red[grp][e]) = a;
-  if (e == 0) {
-    red[grp][D] = m;
-    red[grp][D + 1] = l;
-  }
-  __syncthreads();
-  if (threadIdx.x >= LP) return;
-  m = red[0][D];
-  l = red[0][D + 1];
-  for (int k = 1; k < NG; ++k) {
-    const float om = red[k][D], os = red[k][D + 1];
-    const f32x4_t o = *reinterpret_cast<const f32x4_t*>(&red[k][e]);
-    const float top = fmaxf(m, om), ref = top == -INFINITY ? 0.0f : top;
-    const float fa = __builtin_amdgcn_exp2f(m - ref), fb = __builtin_amdgcn_exp2f(om - ref);
-    m = top;
-    l = l * fa + os * fb;
+    __syncthreads();
+    if (grp > 0) return;
+    for (int k = 1; k < NG; ++k) p.add(red[k][D], red[k][D + 1], *reinterpret_cast<const f32x4_t*>(&red[k][e]));
+  } else {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) a[x] = a[x] * fa + o[x] * fb;
+    for (int d = LP; d < 64; d *= 2) {
+      // both sides add the lower group's result first, so that they agree
+      Partial q{__shfl_xor(p.m, d), __shfl_xor(p.l, d), {}};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) q.a[x] = __shfl_xor(p.a[x], d);
+      if (tid & d) {
+        q.add(p.m, p.l, p.a);
+        p = q;
+      } else {
+        p.add(q.m, q.l, q.a);
+      }
+    }
+    if (grp > 0) return;
   }
-  const float f = l == 0.0f ? 0.0f : 1.0f / l;
-  *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack_bf16x2(a[0] * f, a[1] * f), pack_bf16x2(a[2] * f, a[3] * f));
+  const float f = p.l == 0.0f ? 0.0f : 1.0f / p.l;
+  *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack_bf16x2(p.a[0] * f, p.a[1] * f), pack_bf16x2(p.a[2] * f, p.a[3] * f));
 }
 
 template <int D, int MT>
@@ -788,8 +772,14 @@ hipError_t attend(const KVAttnPlan& pl, const KVCache& c, const KVSeqs& s, const
       pl.solo, fill);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.solo) return e;
-  k_kv_join<D, MT><<<dim3(s.T, Hq), 256, 0, stream>>>(c, s, Hq, static_cast<uint16_t*>(out),
-                                                      static_cast<const float*>(ws), static_cast<int>(pl.workers), fill);
+  const int64_t items = static_cast<int64_t>(s.T) * Hq;
+  uint16_t* o = static_cast<uint16_t*>(out);
+  const float* part = static_cast<const float*>(ws);
+  // 80 rows of 40 heads, 4 or 5 partial results each: 8.1 us with a workgroup a row, 5.5 with a wave
+  if (items <= kWideRows)
+    k_kv_join<D, MT, true><<<static_cast<unsigned>(items), 256, 0, stream>>>(c, s, Hq, o, part, static_cast<int>(pl.workers), fill);
+  else
+    k_kv_join<D, MT, false><<<static_cast<unsigned>((items + 3) / 4), 256, 0, stream>>>(c, s, Hq, o, part, static_cast<int>(pl.workers), fill);
   return hipGetLastError();
 }
 
@@ -838,7 +828,7 @@ KVAttnPlan plan_kv_attention(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int3
   pl.mt = mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
   const int64_t units = (T * G / (16 * pl.mt) + B) * Hkv, steps = (tokens + kStep - 1) / kStep;
   pl.solo = steps <= kSoloSteps;
-  pl.workers = pl.solo ? units : 2 * cus;
+  pl.workers = pl.solo ? units : kWorkers * cus;
   pl.steps = steps > 0 && units > INT64_MAX / steps ? INT64_MAX : units * (steps > 0 ? steps : 1);
   pl.ws_bytes = pl.solo ? 0 : 2 * static_cast<size_t>(pl.workers) * (16 * pl.mt * (D + 2)) * sizeof(float);
   return pl;
