@@ -30,31 +30,39 @@ __device__ __forceinline__ void land() {                       // every copy has
   asm volatile("" ::: "memory");
 }
 
+__device__ __forceinline__ void share_lds() {                  // LDS writes are seen by every wave; copies stay in flight
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // LDS tile of 64 rows: [D / 32 slices of 32 elements][64 rows][64 bytes], the 16-byte chunk c of a row's slice at chunk c ^ ((row >> 2) & 3).
 // Both reads are free of bank conflicts (16 bytes of 8 neighbouring rows; the
 // transposed read's 32 bytes of 8 rows), and slice and row are immediate offsets
 // from two lane addresses each.
 //
 // Copier copies rows row0 .. row0+63 of a sequence of n rows (the last row
-// again behind the end; its scores are masked) into such a tile: a wave copies
-// 16 rows, one slice an instruction.
+// again behind the end; its scores are masked) into such a tile: an
+// instruction copies 16 rows of one slice, 4 or 8 waves share the slices.
 constexpr int kSlice = kTile * 64;                              // bytes
-template <int D>
+template <int D, int WAVES = 4>
 struct Copier {
+  static constexpr int kSlices = D / 32 / (WAVES / 4);          // of one wave
   uint32_t off, stride;                                         // bytes
   int row;
   __device__ __forceinline__ explicit Copier(int64_t stride_elems) {
     const int lane = threadIdx.x & 63;
-    row = 16 * uniform(threadIdx.x >> 6) + (lane >> 2);
+    row = 16 * (uniform(threadIdx.x >> 6) & 3) + (lane >> 2);
     stride = static_cast<uint32_t>(stride_elems) * 2;
     off = 16 * ((lane & 3) ^ ((row >> 2) & 3));
   }
   __device__ __forceinline__ void operator()(const uint16_t* seq, int row0, int n, const void* tile) const {
-    const char* base = reinterpret_cast<const char*>(seq) + static_cast<int64_t>(row0) * stride;
-    const uint32_t lds = lds_addr(tile) + 1024 * uniform(threadIdx.x >> 6);
+    const int wave = uniform(threadIdx.x >> 6), first = WAVES == 4 ? 0 : kSlices * (wave >> 2);
+    const char* base = reinterpret_cast<const char*>(seq) + static_cast<int64_t>(row0) * stride + 64 * first;
+    const uint32_t lds = lds_addr(tile) + 1024 * (wave & 3) + kSlice * first;
     const uint32_t o = static_cast<uint32_t>(min(row, n - 1 - row0)) * stride + off;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) copy16(o, base + 64 * i, lds + kSlice * i);
+    for (int i = 0; i < kSlices; ++i) copy16(o, base + 64 * i, lds + kSlice * i);
   }
 };
 
@@ -79,13 +87,16 @@ struct Offs {
 __device__ __forceinline__ bf16x8_t read_row(const char* tile, const Offs& o, int w, int ks) {
   return *reinterpret_cast<const bf16x8_t*>(tile + (ks >> 1) * kSlice + w * 2048 + o.row[ks & 1]);
 }
+__device__ __forceinline__ bf16x8_t read_tr_at(const char* lo, const char* hi) {
+  const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)lo);
+  const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)hi);
+  const u32x2_t x = __builtin_bit_cast(u32x2_t, a), y = __builtin_bit_cast(u32x2_t, b);
+  return __builtin_bit_cast(bf16x8_t, u32x4_t{x[0], x[1], y[0], y[1]});
+}
 // element 32 dt + (lane & 31) of rows 16 m + 4 h .. +3 and 16 m + 8 + 4 h .. +3
 __device__ __forceinline__ bf16x8_t read_tr(const char* tile, const Offs& o, int m, int dt) {
   const char* p = tile + dt * kSlice + m * 1024;
-  const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + o.tr[0]));
-  const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + o.tr[1]));
-  const u32x2_t x = __builtin_bit_cast(u32x2_t, a), y = __builtin_bit_cast(u32x2_t, b);
-  return __builtin_bit_cast(bf16x8_t, u32x4_t{x[0], x[1], y[0], y[1]});
+  return read_tr_at(p + o.tr[0], p + o.tr[1]);
 }
 __device__ __forceinline__ f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -444,17 +455,25 @@ __global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, GradArgs 
                      pack_bf16x2(acc[dt][4 * b + 2] * a.scale, acc[dt][4 * b + 3] * a.scale));
 }
 
-// grad_k and grad_v: a wave keeps 32 keys with their values and streams the
-// queries and output gradients of every query head of the group, in order.
+// grad_k and grad_v: a workgroup of 8 waves keeps 128 keys with their values
+// and streams the queries and output gradients of every query head of the
+// group, in order, in tiles of 64 rows.
 //   grad_v = P^T dO, grad_k = scale dS^T Q
+// Two waves share 32 keys.  First each forms P and dS of its half of the tile's
+// rows and leaves them in LDS (bf16); then each multiplies the whole tile into
+// its half of the elements of grad_v and grad_k.  So the sums of a wave take 64
+// registers, not 128, and two waves fit a SIMD, one's exponentials under the
+// other's products (8 products a step in 4 waves with 512 registers each:
+// 360 us where this takes KVUS).
 // Where the tiles alone leave compute units idle, the heads of a group are
 // split over `parts` workgroups, whose fp32 sums k_prompt_join adds in order.
 template <int D>
-__global__ __launch_bounds__(256, 1) void k_prompt_bwd_kv(PromptArgs a, GradArgs g, uint16_t* __restrict__ gk,
+__global__ __launch_bounds__(512, 2) void k_prompt_bwd_kv(PromptArgs a, GradArgs g, uint16_t* __restrict__ gk,
                                                           uint16_t* __restrict__ gv, float* __restrict__ part, int parts,
                                                           int bound) {
-  constexpr int KS = D / 16, DT = D / 32;
+  constexpr int KS = D / 16, DT = D / 64;                       // 32-element tiles of a wave's half
   __shared__ __align__(1024) char lds[2][2][kTile * D * 2];     // [buffer][queries, output gradients]
+  __shared__ __align__(1024) char weights[2][kRows * kTile * 2];   // [P, dS][key][row of the tile]
   __shared__ __align__(256) float stat[2][2][kTile];            // [buffer][lse, delta]
   const int x = blockIdx.x % (a.Hkv * parts), z = blockIdx.x / (a.Hkv * parts);
   const int hk = head_of(x / parts, a.Hkv), pt = x % parts;
@@ -467,10 +486,18 @@ __global__ __launch_bounds__(256, 1) void k_prompt_bwd_kv(PromptArgs a, GradArgs
   TileAt at;
   if (!find_tile(a, z, at)) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), l32 = lane & 31, h = lane >> 5;
-  const int k0 = ((at.n + kRows - 1) / kRows - at.weight) * kRows, w0 = k0 + 32 * wave, ki = w0 + l32;
+  const int kg = wave & 3, hf = wave >> 2;
+  const int k0 = ((at.n + kRows - 1) / kRows - at.weight) * kRows, w0 = k0 + 32 * kg, ki = w0 + l32;
   const float c = a.scale * kLog2e;
   const Offs of;
-  const Copier<D> cq(a.q_stride), cg(g.go_stride);
+  int tr[2];                                                    // transposed reads in natural order: rows 8h + i (+ 4)
+#pragma unroll
+  for (int hi = 0; hi < 2; ++hi) {
+    const int r = 8 * h + ((lane & 15) >> 2) + 4 * hi, col = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    tr[hi] = r * 64 + (((col >> 3) ^ ((r >> 2) & 3)) << 4) + (col & 7) * 2 + hf * DT * kSlice;
+  }
+  const int wrow = (32 * kg + l32) * 128;                       // this lane's key in `weights`: 16-byte chunk q / 8 at chunk ^ (key & 7)
+  const Copier<D, 8> cq(a.q_stride), cg(g.go_stride);
   const int j0 = k0 / kTile;                                    // first query tile that sees these keys
   const int per = (at.n + kTile - 1) / kTile - j0;
   const uint16_t* qb = a.q + at.first * a.q_stride + h0 * D;
@@ -498,50 +525,46 @@ __global__ __launch_bounds__(256, 1) void k_prompt_bwd_kv(PromptArgs a, GradArgs
     av[dt] = zero16();
   }
 
-  struct Pair {
-    f32x16_t s, dp;
-  };
-  auto scores = [&](int buf, int w, Pair& p) __attribute__((always_inline)) {
+  auto weigh = [&](int buf, int j, auto masked) __attribute__((always_inline)) {
     const char* qt = lds[buf][0];
     const char* gt = lds[buf][1];
-    p.s = zero16();
-    p.dp = zero16();
+    f32x16_t s = zero16(), dp = zero16();
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      p.s = mfma(read_row(qt, of, w, ks), kf[ks], p.s);
-      p.dp = mfma(read_row(gt, of, w, ks), vf[ks], p.dp);
-    }
-  };
-  auto weigh = [&](int buf, int j, int w, Pair& p, auto masked) __attribute__((always_inline)) {
+    for (int ks = 0; ks < KS; ++ks) s = mfma(read_row(qt, of, hf, ks), kf[ks], s);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) dp = mfma(read_row(gt, of, hf, ks), vf[ks], dp);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      const f32x4_t ls = *reinterpret_cast<const f32x4_t*>(&stat[buf][0][32 * w + 8 * b + 4 * h]);
-      const f32x4_t dl = *reinterpret_cast<const f32x4_t*>(&stat[buf][1][32 * w + 8 * b + 4 * h]);
+      const f32x4_t ls = *reinterpret_cast<const f32x4_t*>(&stat[buf][0][32 * hf + 8 * b + 4 * h]);
+      const f32x4_t dl = *reinterpret_cast<const f32x4_t*>(&stat[buf][1][32 * hf + 8 * b + 4 * h]);
+      float p[4], ds[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 4 * b + i;
-        p.s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(p.s[r], c, -ls[i]));
-        p.dp[r] = p.s[r] * (p.dp[r] - dl[i]);
+        p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, -ls[i]));
+        ds[i] = p[i] * (dp[r] - dl[i]);
         if constexpr (decltype(masked)::value) {
-          const int q = j * kTile + 32 * w + reg_row(r) + 4 * h;
-          if (q < ki || q >= at.n) {
-            p.s[r] = 0.0f;
-            p.dp[r] = 0.0f;
-          }
+          const int q = j * kTile + 32 * hf + reg_row(r) + 4 * h;
+          if (q < ki || q >= at.n) p[i] = ds[i] = 0.0f;
         }
       }
+      const int at_q = wrow + (((4 * hf + b) ^ (l32 & 7)) << 4) + 8 * h;
+      *reinterpret_cast<uint2*>(weights[0] + at_q) = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
+      *reinterpret_cast<uint2*>(weights[1] + at_q) = make_uint2(pack_bf16x2(ds[0], ds[1]), pack_bf16x2(ds[2], ds[3]));
     }
   };
-  auto gather = [&](int buf, int w, const Pair& p) __attribute__((always_inline)) {
-    const char* qt = lds[buf][0];
-    const char* gt = lds[buf][1];
+  auto gather = [&](int buf, int w) __attribute__((always_inline)) {
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const bf16x8_t pf = pack8(p.s, m), sf = pack8(p.dp, m);
+    for (int m = 2 * w; m < 2 * w + 2; ++m) {
+      const int at_q = wrow + (((2 * m + h) ^ (l32 & 7)) << 4);
+      const bf16x8_t pf = *reinterpret_cast<const bf16x8_t*>(weights[0] + at_q);
+      const bf16x8_t sf = *reinterpret_cast<const bf16x8_t*>(weights[1] + at_q);
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) {
-        av[dt] = mfma(read_tr(gt, of, 2 * w + m, dt), pf, av[dt]);
-        ak[dt] = mfma(read_tr(qt, of, 2 * w + m, dt), sf, ak[dt]);
+        const char* q = lds[buf][0] + m * 1024 + dt * kSlice;
+        const char* o = lds[buf][1] + m * 1024 + dt * kSlice;
+        av[dt] = mfma(read_tr_at(o + tr[0], o + tr[1]), pf, av[dt]);
+        ak[dt] = mfma(read_tr_at(q + tr[0], q + tr[1]), sf, ak[dt]);
       }
     }
   };
@@ -565,23 +588,22 @@ __global__ __launch_bounds__(256, 1) void k_prompt_bwd_kv(PromptArgs a, GradArgs
       }
       land();
       if (st + 1 < steps) copy_step(buf ^ 1, i, tile_of(k));
-      // one half's weights are computed under the other half's products
-      Pair p0, p1;
-      scores(buf, 0, p0);
-      scores(buf, 1, p1);
-      weigh(buf, j, 0, p0, masked);
-      gather(buf, 0, p0);
-      weigh(buf, j, 1, p1, masked);
-      gather(buf, 1, p1);
+      // rows before every key of a wave have no weights: neither formed nor read
+      if (!decltype(masked)::value || j * kTile + 32 * hf + 31 >= w0) weigh(buf, j, masked);
+      share_lds();
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        if (!decltype(masked)::value || j * kTile + 32 * w + 31 >= w0) gather(buf, w);
     }
     land();                                                     // the tiles are free again
   };
   sweep(front + edge, 0, std::true_type{});
   sweep(inner, front, std::false_type{});
   if (ki >= at.n) return;
+  const int64_t at_out = (t * a.Hkv + hk) * D + 32 * DT * hf + 4 * h;
   if (parts > 1) {
     const int64_t set = static_cast<int64_t>(a.T) * a.Hkv * D;
-    float* dst = part + 2 * pt * set + (t * a.Hkv + hk) * D + 4 * h;
+    float* dst = part + 2 * pt * set + at_out;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
@@ -591,16 +613,14 @@ __global__ __launch_bounds__(256, 1) void k_prompt_bwd_kv(PromptArgs a, GradArgs
       }
     return;
   }
-  uint16_t* dk = gk + (t * a.Hkv + hk) * D + 4 * h;
-  uint16_t* dv = gv + (t * a.Hkv + hk) * D + 4 * h;
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      *reinterpret_cast<uint2*>(dk + 32 * dt + 8 * b) =
+      *reinterpret_cast<uint2*>(gk + at_out + 32 * dt + 8 * b) =
           make_uint2(pack_bf16x2(ak[dt][4 * b] * a.scale, ak[dt][4 * b + 1] * a.scale),
                      pack_bf16x2(ak[dt][4 * b + 2] * a.scale, ak[dt][4 * b + 3] * a.scale));
-      *reinterpret_cast<uint2*>(dv + 32 * dt + 8 * b) =
+      *reinterpret_cast<uint2*>(gv + at_out + 32 * dt + 8 * b) =
           make_uint2(pack_bf16x2(av[dt][4 * b], av[dt][4 * b + 1]), pack_bf16x2(av[dt][4 * b + 2], av[dt][4 * b + 3]));
     }
 }
@@ -658,7 +678,7 @@ hipError_t backward(const PromptArgs& a, const GradArgs& g, void* gq, void* gk, 
   if (e != hipSuccess) return e;
   const int parts = head_parts(a.T, a.B, a.Hq, a.Hkv, device_cu_count());
   float* part = g.stat + stat_floats(a.T, a.Hq);
-  k_prompt_bwd_kv<D><<<static_cast<unsigned>(bound) * a.Hkv * parts, 256, 0, stream>>>(
+  k_prompt_bwd_kv<D><<<static_cast<unsigned>(bound) * a.Hkv * parts, 512, 0, stream>>>(
       a, g, static_cast<uint16_t*>(gk), static_cast<uint16_t*>(gv), part, parts, bound);
   e = hipGetLastError();
   if (e != hipSuccess || parts == 1) return e;
