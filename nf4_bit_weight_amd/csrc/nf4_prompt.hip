@@ -188,6 +188,39 @@ __device__ __forceinline__ void fill_rows(const PromptArgs& a, uint16_t* out, in
   }
 }
 
+// This thread's share of an LDS tile, read ahead; take_out then sets its
+// elements that are infinite or NaN to zero, and *found if there were any (every
+// thread of the workgroup takes part).
+template <int D>
+struct TileShare {
+  static constexpr int kN = kTile * D * 2 / 4096;
+  u32x4_t x[kN];
+  __device__ __forceinline__ explicit TileShare(const char* tile) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) x[i] = reinterpret_cast<const u32x4_t*>(tile)[i * 256 + threadIdx.x];
+  }
+  __device__ __forceinline__ void take_out(char* tile, int* found) {
+    uint32_t most = 0;                                          // largest magnitude: odd elements shifted up, even ones as they are
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) most = max(most, max(x[i][k] & 0x7FFF0000u, x[i][k] << 16 & 0x7FFF0000u));
+    if (most >= 0x7F800000u) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if ((x[i][k] & 0x7F80u) == 0x7F80u) x[i][k] &= 0xFFFF0000u;
+          if ((x[i][k] & 0x7F800000u) == 0x7F800000u) x[i][k] &= 0xFFFFu;
+        }
+        reinterpret_cast<u32x4_t*>(tile)[i * 256 + threadIdx.x] = x[i];
+      }
+      *found = 1;
+    }
+    share_lds();
+  }
+};
+
 // Heads of one key head next to each other in one XCD's queue (workgroups go
 // round the 8 XCDs in order), so that they share its L2.
 __device__ __forceinline__ int head_of(int x, int heads) { return heads % 8 == 0 ? (x % 8) * (heads / 8) + x / 8 : x; }
@@ -204,6 +237,7 @@ __global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* _
                                                        uint16_t* __restrict__ rest, float* __restrict__ lse, int bound) {
   constexpr int KS = D / 16, DT = D / 32;
   __shared__ __align__(1024) char lds[2][2][kTile * D * 2];     // [buffer][keys, values]
+  __shared__ int odd[2];                                        // of the tiles on the diagonal: values that are no numbers
   const int x = blockIdx.x % a.Hq, z = blockIdx.x / a.Hq;
   const int hq = head_of(x, a.Hq), hk = hq / (a.Hq / a.Hkv);
   fill_rows(a, out, a.Hq, hq, z, bound);
@@ -284,6 +318,7 @@ __global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* _
     if (j + 1 < tiles) cv(vb, (j + 1) * kTile, at.n, lds[(j + 1) & 1][1]);
   };
   f32x16_t s0[2], s1[2];
+  if (threadIdx.x < 2) odd[threadIdx.x] = 0;
   land();
   if (1 < tiles) ck(kb, kTile, at.n, lds[1][0]);
   cv(vb, 0, at.n, lds[0][1]);
@@ -300,14 +335,34 @@ __global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* _
   }
   for (int j = whole; j < tiles; ++j) {                         // at most two, on the diagonal
     advance(j);
-    if (j * kTile > w0 + 31) continue;                          // behind every row of this wave
+    // A value that is no number must not reach the rows before its token
+    // through a weight of zero: it is taken out of the tile here and added to
+    // the rows that see it below.
+    TileShare<D> values(lds[j & 1][1]);
+    const bool some = j * kTile <= w0 + 31;                     // else the tile lies behind every row of this wave
+    if (some) {
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+      for (int w = 0; w < 2; ++w)
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (j * kTile + 32 * w + reg_row(r) + 4 * h > qi) s0[w][r] = -INFINITY;
-    maximum(s0);
+        for (int r = 0; r < 16; ++r)
+          if (j * kTile + 32 * w + reg_row(r) + 4 * h > qi) s0[w][r] = -INFINITY;
+      maximum(s0);
+    }
+    values.take_out(lds[j & 1][1], &odd[j - whole]);
+    if (!some) continue;
     weigh(j, s0);
+    if (odd[j - whole]) {
+      for (int key = j * kTile; key < min(at.n, min(j * kTile + kTile, w0 + 32)); ++key) {
+        const uint16_t* v = vb + key * a.v_stride + 4 * h;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const uint32_t x = v[32 * dt + reg_row(r)];
+            if ((x & 0x7F80u) == 0x7F80u && key <= qi) acc[dt][r] += __builtin_bit_cast(float, x << 16);
+          }
+      }
+    }
     if (j + 1 < tiles) scores(j + 1, s0);
   }
   const float total = half_sum(sum[0] + sum[1]);

@@ -127,6 +127,30 @@ def test_large_scores():
     R.within(out, *R.prompt(q, k, v, lens, 0.125)["out"], "large scores")
 
 
+@pytest.mark.parametrize("at", [0, 40, 63, 64, 100, 199])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_odd_values_reach_only_their_readers(at, value):
+    """A key or value that is no number leaves the rows before its token alone."""
+    lens, D = [200], 128
+    _, q, k, v = inputs(lens, 2, 1, D, seed=6)
+    want, bound = R.prompt(q, k, v, lens, float(np.float32(D ** -0.5)))["out"]
+    off = R.offsets_of(lens).to(DEV)
+    v2 = v.clone()
+    v2[at, 0, 5] = value
+    out = nf4_prompt_attention(q.to(DEV), k.to(DEV), v2.to(DEV), off)
+    R.within(out[:at], want[:at], bound[:at], "rows before")
+    assert not torch.isfinite(out[at:, :, 5]).any()
+    other = torch.arange(D) != 5
+    R.within(out[:, :, other.to(DEV)], want[:, :, other], bound[:, :, other], "other elements")
+    if value > 0:
+        assert (out[at:, :, 5] == value).all()
+    k2 = k.clone()
+    k2[at, 0, 7] = float("nan")
+    out = nf4_prompt_attention(q.to(DEV), k2.to(DEV), v.to(DEV), off)
+    R.within(out[:at], want[:at], bound[:at], "rows before")
+    assert torch.isnan(out[at:]).all()
+
+
 def test_rows_outside_sequences():
     """Padding that holds NaN reaches nothing; its results are zeros in fresh
     tensors, and as they were in one passed in."""
