@@ -13,5 +13,5 @@ from .api import (NF4Weight, nf4_dequantize, nf4_grouped_matmul_bwd_input,  # no
                   nf4_path_counts, nf4_quantize, nf4_reset_path_counts, nf4_workspace_bytes)
 from .attention import (NF4KVCache, nf4_kv_append, nf4_kv_attention, nf4_kv_attention_workspace,  # noqa: F401
                         nf4_kv_cache, nf4_kv_dequantize, nf4_prompt_attention_bwd, nf4_prompt_attention_fwd)
-from .autograd import (NF4GroupedMatMul, NF4MatMul, NF4PromptAttention, nf4_grouped_linear,  # noqa: F401
-                       nf4_linear, nf4_prompt_attention)
+from .autograd import (NF4GroupedMatMul, NF4MatMul, nf4_grouped_linear, nf4_linear,  # noqa: F401
+                       nf4_prompt_attention)

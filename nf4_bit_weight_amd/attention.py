@@ -44,7 +44,8 @@ def _call(name: str, *args):
     return r
 
 
-_C_NAMES = {"prompt_fwd": "prompt_attention_fwd", "prompt_bwd": "prompt_attention_bwd"}
+_C_NAMES = {"prompt_fwd": "prompt_attention_fwd", "prompt_bwd": "prompt_attention_bwd",
+            "prompt_attention": "prompt_attention_fwd"}
 
 
 @dataclass

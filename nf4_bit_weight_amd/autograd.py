@@ -24,8 +24,6 @@ from __future__ import annotations
 
 import torch
 
-from torch.autograd.function import once_differentiable
-
 from . import api, attention
 from .api import NF4Weight
 
@@ -102,44 +100,12 @@ def nf4_grouped_linear(x: torch.Tensor, offsets: torch.Tensor, w: NF4Weight, E: 
     return NF4GroupedMatMul.apply(x, offsets, *w.tensors(), E, w.N, w.K, w.bits)
 
 
-class NF4PromptAttention(torch.autograd.Function):
-    """Causal attention over packed sequences, differentiable in q, k and v.
-    Saved are the bf16 operands, the output with what its rounding took, and
-    each row's log-sum-exp."""
-
-    @staticmethod
-    def forward(ctx, q, k, v, offsets, scale):
-        q2, k2, v2 = (_head_rows(t) for t in (q, k, v))
-        out, rest, lse = attention.nf4_prompt_attention_fwd(q2, k2, v2, offsets, scale, for_backward=True)
-        ctx.save_for_backward(q2, k2, v2, out, rest, lse, offsets)
-        ctx.scale = scale
-        ctx.dtypes = (q.dtype, k.dtype, v.dtype)
-        return out.to(q.dtype)
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, grad_out):
-        q, k, v, out, rest, lse, offsets = ctx.saved_tensors
-        grads = attention.nf4_prompt_attention_bwd(_head_rows(grad_out), q, k, v, out, rest, lse, offsets, ctx.scale)
-        return (*(g.to(d) if need else None for g, d, need in zip(grads, ctx.dtypes, ctx.needs_input_grad)), None, None)
-
-
-def _head_rows(t: torch.Tensor) -> torch.Tensor:
-    """t [T, heads, D] as the kernels take it: bf16, the heads of a row
-    contiguous, rows 16-byte aligned."""
-    t = t if t.dtype == torch.bfloat16 else t.to(torch.bfloat16)
-    if t.dim() != 3 or t.numel() == 0:
-        return t
-    fits = (t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == t.shape[2])
-            and (t.shape[0] == 1 or t.stride(0) % 8 == 0) and t.data_ptr() % 16 == 0)
-    return t if fits else t.clone(memory_format=torch.contiguous_format)
-
-
 def nf4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor,
                          scale: float = None) -> torch.Tensor:
     """Causal attention inside each of the packed sequences that offsets
-    (int32 [B + 1]) cut q [T, Hq, D] and k, v [T, Hkv, D] into; differentiable."""
-    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
-        return NF4PromptAttention.apply(q, k, v, offsets, scale)
-    out = attention.nf4_prompt_attention_fwd(_head_rows(q), _head_rows(k), _head_rows(v), offsets, scale)
-    return out if out.dtype == q.dtype else out.to(q.dtype)
+    (int32 [B + 1]) cut q [T, Hq, D] and k, v [T, Hkv, D] into; differentiable in
+    q, k and v, once.  The kernels compute in bf16 with fp32 accumulation; the
+    output and the gradients come back in the dtypes that the caller passed in.
+    Rows outside every sequence are zeros in both.  (The autograd node is in
+    csrc/nf4_torch.cpp and saves tensors only, through save_for_backward.)"""
+    return attention._call("prompt_attention", q, k, v, offsets, scale)

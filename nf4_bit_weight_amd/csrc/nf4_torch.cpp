@@ -1,6 +1,6 @@
 // Argument marshalling of the attention calls (nf4_attn.h) for Python: checks of
 // tensors, allocation of results and workspaces, the current stream of the
-// tensors' device, and the C call.  The kernels of a decode step take a few
+// tensors' device, the C call, and the autograd node of the prompt's attention.  The kernels of a decode step take a few
 // microseconds, less than the same checks take in the interpreter.  Nothing
 // here computes.
 //
@@ -13,9 +13,11 @@
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <optional>
 #include <sstream>
 #include <stdexcept>
 #include <string>
@@ -115,8 +117,7 @@ struct Rows {
   int32_t H = 0;
 };
 // A [T, heads, D] bf16 tensor whose rows may be strided.
-Rows rows_of(PyObject* o, const char* name, int64_t heads, int64_t D, int64_t T, const c10::Device& dev) {
-  const Tensor& t = tensor(o, name);
+Rows rows_of(const Tensor& t, const char* name, int64_t heads, int64_t D, int64_t T, const c10::Device& dev) {
   if (t.dim() != 3 || t.size(2) != D || (heads >= 0 && t.size(1) != heads))
     refuse(name, " must be [T, ", heads >= 0 ? std::to_string(heads) : "heads", ", ", D, "], got ", t.sizes());
   if (T >= 0 && t.size(0) != T) refuse(name, " has ", t.size(0), " rows, expected ", T);
@@ -130,6 +131,10 @@ Rows rows_of(PyObject* o, const char* name, int64_t heads, int64_t D, int64_t T,
     refuse(name, ": the heads of a row must be contiguous and rows a multiple of 8 elements apart");
   if (r.T > 1) r.stride = t.stride(0);
   return r;
+}
+
+Rows rows_of(PyObject* o, const char* name, int64_t heads, int64_t D, int64_t T, const c10::Device& dev) {
+  return rows_of(tensor(o, name), name, heads, D, T, dev);
 }
 
 int32_t groups(int64_t Hq, int64_t H) {
@@ -149,12 +154,11 @@ Tensor result(PyObject* o, const char* name, int64_t T, int64_t H, int64_t D, co
   need(t, name, at::kBFloat16, T * H * D, &dev);
   return t;
 }
-// The caller's workspace, or a new one.
-Tensor workspace(PyObject* o, size_t bytes, const c10::Device& dev) {
-  if (!given(o)) {
-    if (bytes == SIZE_MAX) bytes = 0;                          // the call itself says why
-    return bytes ? fresh({static_cast<int64_t>(bytes)}, at::kByte, dev) : Tensor();
-  }
+Tensor new_workspace(size_t bytes, const c10::Device& dev) {
+  if (bytes == SIZE_MAX) bytes = 0;                            // the call itself says why
+  return bytes ? fresh({static_cast<int64_t>(bytes)}, at::kByte, dev) : Tensor();
+}
+Tensor given_workspace(PyObject* o, const c10::Device& dev) {
   const Tensor& t = tensor(o, "ws");
   if (!t.is_cuda()) refuse("ws must be a device tensor");
   if (!t.is_contiguous()) refuse("ws must be contiguous");
@@ -163,15 +167,18 @@ Tensor workspace(PyObject* o, size_t bytes, const c10::Device& dev) {
 }
 void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
-float scale_of(PyObject* o, int32_t D) {
-  double s = 1.0 / std::sqrt(static_cast<double>(D));
-  if (given(o)) {
-    s = PyFloat_AsDouble(o);
-    if (PyErr_Occurred()) {
-      PyErr_Clear();
-      refuse("scale must be a number");
-    }
+using Scale = std::optional<double>;
+Scale scale_arg(PyObject* o) {
+  if (!given(o)) return {};
+  const double s = PyFloat_AsDouble(o);
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    refuse("scale must be a number");
   }
+  return s;
+}
+float scale_of(const Scale& given_scale, int32_t D) {
+  const double s = given_scale ? *given_scale : 1.0 / std::sqrt(static_cast<double>(D));
   const float f = static_cast<float>(s);
   if (!(f > 0.0f) || !std::isfinite(f)) refuse("scale must be positive and finite, got ", s);
   return f;
@@ -269,12 +276,12 @@ PyObject* kv_attention(PyObject* const* a) {
   const Rows q = rows_of(a[4], "q", -1, c.D, -1, c.dev);
   const int32_t Hq = groups(q.H, c.H);
   const Seqs s = seqs_of(a[5], a[6], a[7], q.T, c.dev);
-  const float scale = scale_of(a[8], c.D);
+  const float scale = scale_of(scale_arg(a[8]), c.D);
   bool fill;
   const Tensor out = result(a[9], "out", q.T, Hq, c.D, c.dev, fill);
   const On on(c.dev);
-  const Tensor ws = workspace(
-      a[10], given(a[10]) ? 0 : nf4_kv_attention_workspace(q.T, s.B, Hq, c.H, c.D, s.width, c.page), c.dev);
+  const Tensor ws = given(a[10]) ? given_workspace(a[10], c.dev)
+                                 : new_workspace(nf4_kv_attention_workspace(q.T, s.B, Hq, c.H, c.D, s.width, c.page), c.dev);
   const int st = nf4_kv_attention(q.p, q.stride, q.T, Hq, SEQ_ARGS(s), CACHE_ARGS(c), scale, ptr(out), fill, ptr(ws),
                                   ws.defined() ? ws.nbytes() : 0, on.stream);
   return st ? PyLong_FromLong(st) : wrap(out);
@@ -287,29 +294,53 @@ struct Prompt {
   const int32_t* offsets = nullptr;
   float scale = 0.0f;
 };
-Prompt prompt_of(PyObject* q, PyObject* k, PyObject* v, PyObject* offsets, PyObject* scale) {
+Prompt prompt_of(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& offsets, const Scale& scale) {
   Prompt p;
-  const Tensor& t = tensor(q, "q");
-  if (t.dim() != 3 || (t.size(2) != 64 && t.size(2) != 128)) refuse("q must be [T, Hq, D] with D 64 or 128, got ", t.sizes());
-  p.dev = t.device();
-  p.D = static_cast<int32_t>(t.size(2));
+  if (q.dim() != 3 || (q.size(2) != 64 && q.size(2) != 128)) refuse("q must be [T, Hq, D] with D 64 or 128, got ", q.sizes());
+  p.dev = q.device();
+  p.D = static_cast<int32_t>(q.size(2));
   p.q = rows_of(q, "q", -1, p.D, -1, p.dev);
   p.k = rows_of(k, "k", -1, p.D, p.q.T, p.dev);
   p.v = rows_of(v, "v", p.k.H, p.D, p.q.T, p.dev);
   groups(p.q.H, p.k.H);
-  const Tensor& off = tensor(offsets, "offsets");
-  need(off, "offsets", at::kInt, -1, &p.dev);
-  if (off.dim() != 1 || off.numel() < 1 || off.numel() > INT32_MAX) refuse("offsets must be [B + 1]");
-  p.B = static_cast<int32_t>(off.numel() - 1);
-  p.offsets = off.data_ptr<int32_t>();
+  need(offsets, "offsets", at::kInt, -1, &p.dev);
+  if (offsets.dim() != 1 || offsets.numel() < 1 || offsets.numel() > INT32_MAX) refuse("offsets must be [B + 1]");
+  p.B = static_cast<int32_t>(offsets.numel() - 1);
+  p.offsets = offsets.data_ptr<int32_t>();
   p.scale = scale_of(scale, p.D);
   return p;
 }
 #define PROMPT_ARGS(p) p.q.p, p.q.stride, p.k.p, p.k.stride, p.v.p, p.v.stride
 
+int run_forward(const Prompt& p, const Tensor& out, const Tensor& rest, const Tensor& lse, bool fill) {
+  const On on(p.dev);
+  return nf4_prompt_attention_fwd(PROMPT_ARGS(p), p.q.T, p.offsets, p.B, p.q.H, p.k.H, p.D, p.scale, ptr(out), ptr(rest),
+                                  static_cast<float*>(ptr(lse)), fill, on.stream);
+}
+struct Grads {
+  Tensor q, k, v;
+};
+int run_backward(const Prompt& p, const Tensor& grad_out, const Tensor& out, const Tensor& rest, const Tensor& lse, PyObject* ws_arg,
+             Grads& grads) {
+  const int64_t T = p.q.T, n = T * p.q.H * p.D;
+  const Rows g = rows_of(grad_out, "grad_out", p.q.H, p.D, T, p.dev);
+  need(out, "out", at::kBFloat16, n, &p.dev);
+  if (rest.defined()) need(rest, "out_rest", at::kBFloat16, n, &p.dev);
+  need(lse, "lse", at::kFloat, T * p.q.H, &p.dev);
+  grads = Grads{fresh({T, p.q.H, p.D}, at::kBFloat16, p.dev), fresh({T, p.k.H, p.D}, at::kBFloat16, p.dev),
+                fresh({T, p.k.H, p.D}, at::kBFloat16, p.dev)};
+  const On on(p.dev);
+  const bool own = !ws_arg || !given(ws_arg);
+  const size_t bytes = nf4_prompt_attention_bwd_workspace(T, p.B, p.q.H, p.k.H, p.D);
+  const Tensor ws = own ? new_workspace(bytes, p.dev) : given_workspace(ws_arg, p.dev);
+  return nf4_prompt_attention_bwd(g.p, g.stride, PROMPT_ARGS(p), out.data_ptr(), ptr(rest), lse.data_ptr<float>(), T,
+                                  p.offsets, p.B, p.q.H, p.k.H, p.D, p.scale, ptr(grads.q), ptr(grads.k), ptr(grads.v), 1,
+                                  ptr(ws), ws.defined() ? ws.nbytes() : 0, on.stream);
+}
+
 // (q, k, v, offsets, scale, out, for_backward)
 PyObject* prompt_fwd(PyObject* const* a) {
-  const Prompt p = prompt_of(a[0], a[1], a[2], a[3], a[4]);
+  const Prompt p = prompt_of(tensor(a[0], "q"), tensor(a[1], "k"), tensor(a[2], "v"), tensor(a[3], "offsets"), scale_arg(a[4]));
   bool fill;
   const Tensor out = result(a[5], "out", p.q.T, p.q.H, p.D, p.dev, fill);
   Tensor rest, lse;
@@ -318,36 +349,83 @@ PyObject* prompt_fwd(PyObject* const* a) {
     rest = fresh({p.q.T, p.q.H, p.D}, at::kBFloat16, p.dev);
     lse = fresh({p.q.H, p.q.T}, at::kFloat, p.dev);
   }
-  const On on(p.dev);
-  const int st = nf4_prompt_attention_fwd(PROMPT_ARGS(p), p.q.T, p.offsets, p.B, p.q.H, p.k.H, p.D, p.scale, ptr(out),
-                                          ptr(rest), static_cast<float*>(ptr(lse)), fill, on.stream);
+  const int st = run_forward(p, out, rest, lse, fill);
   if (st) return PyLong_FromLong(st);
   return keep ? several(out, rest, lse) : wrap(out);
 }
 
 // (grad_out, q, k, v, out, out_rest, lse, offsets, scale, ws)
 PyObject* prompt_bwd(PyObject* const* a) {
-  const Prompt p = prompt_of(a[1], a[2], a[3], a[7], a[8]);
-  const int64_t T = p.q.T, n = T * p.q.H * p.D;
-  const Rows g = rows_of(a[0], "grad_out", p.q.H, p.D, T, p.dev);
-  const Tensor &out = tensor(a[4], "out"), &lse = tensor(a[6], "lse");
-  need(out, "out", at::kBFloat16, n, &p.dev);
-  const void* rest = nullptr;
-  if (given(a[5])) {
-    const Tensor& t = tensor(a[5], "out_rest");
-    need(t, "out_rest", at::kBFloat16, n, &p.dev);
-    rest = t.data_ptr();
+  const Prompt p = prompt_of(tensor(a[1], "q"), tensor(a[2], "k"), tensor(a[3], "v"), tensor(a[7], "offsets"), scale_arg(a[8]));
+  Grads g;
+  const int st = run_backward(p, tensor(a[0], "grad_out"), tensor(a[4], "out"), given(a[5]) ? tensor(a[5], "out_rest") : Tensor(),
+                          tensor(a[6], "lse"), a[9], g);
+  return st ? PyLong_FromLong(st) : several(g.q, g.k, g.v);
+}
+
+// t [T, heads, D] as the kernels take it: bf16, the heads of a row contiguous,
+// rows 16-byte aligned.
+Tensor head_rows(const Tensor& t) {
+  const Tensor x = t.scalar_type() == at::kBFloat16 ? t : t.to(at::kBFloat16);
+  if (x.dim() != 3 || x.numel() == 0) return x;
+  const bool fits = x.stride(2) == 1 && (x.size(1) == 1 || x.stride(1) == x.size(2)) &&
+                    (x.size(0) == 1 || x.stride(0) % 8 == 0) && reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0;
+  return fits ? x : x.clone(at::MemoryFormat::Contiguous);
+}
+void ok(int status, const char* name) {
+  if (status) throw std::runtime_error(std::string(name) + " failed: " + nf4_status_str(status));
+}
+
+// Causal attention over packed sequences, differentiable in q, k and v.  Saved
+// are the bf16 operands, the output with what its rounding took, and each
+// row's log-sum-exp: tensors only, through save_for_backward, so that saved-tensor
+// hooks and activation checkpointing see them.  (A node in C++: its backward
+// runs on autograd's thread without the interpreter.)
+struct PromptAttention : torch::autograd::Function<PromptAttention> {
+  static Tensor forward(torch::autograd::AutogradContext* ctx, const Tensor& q, const Tensor& k, const Tensor& v,
+                        const Tensor& offsets, double scale) {
+    const Tensor q2 = head_rows(q), k2 = head_rows(k), v2 = head_rows(v);
+    const Prompt p = prompt_of(q2, k2, v2, offsets, scale);
+    const Tensor out = fresh({p.q.T, p.q.H, p.D}, at::kBFloat16, p.dev), rest = fresh({p.q.T, p.q.H, p.D}, at::kBFloat16, p.dev),
+                 lse = fresh({p.q.H, p.q.T}, at::kFloat, p.dev);
+    ok(run_forward(p, out, rest, lse, true), "nf4_prompt_attention_fwd");
+    ctx->save_for_backward({q2, k2, v2, out, rest, lse, offsets});
+    ctx->saved_data["scale"] = scale;
+    ctx->saved_data["q"] = q.scalar_type();
+    ctx->saved_data["k"] = k.scalar_type();
+    ctx->saved_data["v"] = v.scalar_type();
+    return out.to(q.scalar_type());
   }
-  need(lse, "lse", at::kFloat, T * p.q.H, &p.dev);
-  const Tensor gq = fresh({T, p.q.H, p.D}, at::kBFloat16, p.dev), gk = fresh({T, p.k.H, p.D}, at::kBFloat16, p.dev),
-               gv = fresh({T, p.k.H, p.D}, at::kBFloat16, p.dev);
-  const On on(p.dev);
-  const Tensor ws =
-      workspace(a[9], given(a[9]) ? 0 : nf4_prompt_attention_bwd_workspace(T, p.B, p.q.H, p.k.H, p.D), p.dev);
-  const int st = nf4_prompt_attention_bwd(g.p, g.stride, PROMPT_ARGS(p), out.data_ptr(), rest, lse.data_ptr<float>(), T,
-                                          p.offsets, p.B, p.q.H, p.k.H, p.D, p.scale, ptr(gq), ptr(gk), ptr(gv), 1,
-                                          ptr(ws), ws.defined() ? ws.nbytes() : 0, on.stream);
-  return st ? PyLong_FromLong(st) : several(gq, gk, gv);
+  static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx, torch::autograd::variable_list grad) {
+    if (at::GradMode::is_enabled())
+      throw std::runtime_error("nf4_prompt_attention: its backward pass is not differentiable (create_graph)");
+    const auto s = ctx->get_saved_variables();
+    const Prompt p = prompt_of(s[0], s[1], s[2], s[6], ctx->saved_data["scale"].toDouble());
+    Grads g;
+    ok(run_backward(p, head_rows(grad[0]), s[3], s[4], s[5], nullptr, g), "nf4_prompt_attention_bwd");
+    auto as = [&](const char* name, const Tensor& x, int i) {
+      return ctx->needs_input_grad(i) ? x.to(ctx->saved_data[name].toScalarType()) : Tensor();
+    };
+    return {as("q", g.q, 0), as("k", g.k, 1), as("v", g.v, 2), Tensor(), Tensor()};
+  }
+};
+
+// (q, k, v, offsets, scale): any floating dtype and layout, differentiable
+PyObject* prompt_attention(PyObject* const* a) {
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &offsets = tensor(a[3], "offsets");
+  for (const Tensor* t : {&q, &k, &v})
+    if (!t->is_cuda()) refuse("q, k and v must be device tensors");
+  if (q.dim() != 3) refuse("q must be [T, Hq, D] with D 64 or 128, got ", q.sizes());
+  const Scale given_scale = scale_arg(a[4]);
+  if (at::GradMode::is_enabled() && (q.requires_grad() || k.requires_grad() || v.requires_grad())) {
+    const double scale = given_scale ? *given_scale : 1.0 / std::sqrt(static_cast<double>(q.size(2)));
+    return wrap(PromptAttention::apply(q, k, v, offsets, scale));
+  }
+  const Tensor q2 = head_rows(q), k2 = head_rows(k), v2 = head_rows(v);
+  const Prompt p = prompt_of(q2, k2, v2, offsets, given_scale);
+  const Tensor out = fresh({p.q.T, p.q.H, p.D}, at::kBFloat16, p.dev);
+  const int st = run_forward(p, out, Tensor(), Tensor(), true);
+  return st ? PyLong_FromLong(st) : wrap(out.to(q.scalar_type()));
 }
 
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -373,7 +451,7 @@ PyMethodDef method(const char* name) {
 PyMethodDef methods[] = {
     method<kv_append, 15>("kv_append"),   method<kv_dequantize, 10>("kv_dequantize"),
     method<kv_attention, 11>("kv_attention"), method<prompt_fwd, 7>("prompt_fwd"),
-    method<prompt_bwd, 10>("prompt_bwd"), {nullptr, nullptr, 0, nullptr},
+    method<prompt_bwd, 10>("prompt_bwd"), method<prompt_attention, 5>("prompt_attention"), {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_nf4_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -235,6 +235,28 @@ def test_shared_leaf_and_checkpoint():
     assert torch.equal(gc, g)
 
 
+def test_saved_tensors_and_second_order():
+    """What the node saves goes through the saved-tensor hooks, an operand
+    changed in place is noticed, and a second derivative is refused."""
+    lens = [20]
+    off = R.offsets_of(lens).to(DEV)
+    xs = [R.normal(i, 20, 2, 64).to(DEV).requires_grad_() for i in range(3)]
+    seen = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: (seen.append(t.shape), t.clone())[1], lambda t: t):
+        out = nf4_prompt_attention(*xs, off)
+    assert len(seen) == 7
+    ref = torch.autograd.grad(nf4_prompt_attention(*xs, off), xs, torch.ones_like(out))
+    assert all(torch.equal(a, b) for a, b in zip(torch.autograd.grad(out, xs, torch.ones_like(out)), ref))
+    out = nf4_prompt_attention(*xs, off)
+    with pytest.raises(RuntimeError, match="not differentiable"):
+        torch.autograd.grad(out, xs, torch.ones_like(out), create_graph=True)
+    out = nf4_prompt_attention(*xs, off)
+    with torch.no_grad():
+        xs[1].add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+
+
 def test_repeatable_and_streams():
     lens = [300, 1, 500]
     _, q, k, v = inputs(lens, 8, 2, 128, seed=2)
