@@ -21,7 +21,8 @@
  *
  * Sequences.  offsets int32 [B + 1] as in the grouped calls of nf4.h: rows
  * offsets[b] .. offsets[b+1]-1 belong to sequence b, non-decreasing, empty
- * sequences allowed.  For the cache calls NULL means one row per sequence
+ * sequences allowed (offsets that overlap or leave 0 .. T give wrong rows, but
+ * no access out of range).  For the cache calls NULL means one row per sequence
  * (T == B).  Rows outside every sequence (padding behind the last one) are
  * left as they were where fill_outside is 0 and written as zeros where it is 1;
  * they are never read.
@@ -38,6 +39,9 @@
  * 6 x / top, half-way outwards (away from zero); a value is level * scale.  A
  * block with top < 2^-120 is kept as zeros (scale 0); one that holds a NaN or
  * an infinity is kept as NaN (scale NaN, patterns 0).
+ *
+ * A workspace belongs to one call at a time: calls that may overlap (other
+ * streams, graphs replayed side by side) take different ones.
  *
  * Page table int32 [B, width], row b's entry i holding tokens i * page ..
  * of sequence b.  lengths int32 [B] counts the tokens of each sequence WITH the

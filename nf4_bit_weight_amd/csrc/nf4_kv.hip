@@ -169,7 +169,8 @@ __global__ __launch_bounds__(256) void k_kv_append(KVCache c, KVSeqs s, AppendAr
 }
 
 // ---- read back ---------------------------------------------------------------
-// 8 elements a thread: one dword of patterns, four hardware conversions.
+// 8 elements a thread: one dword of patterns, four hardware conversions.  Bound
+// by memory: 17616 rows of 8 heads in 22 us (92 MB, 4.2 TB/s).
 template <int D, int TT>
 __global__ __launch_bounds__(256) void k_kv_dequantize(KVCache c, KVSeqs s, uint16_t* k_out, uint16_t* v_out, int fill) {
   constexpr int D8 = D / 8, kPer = TT * D8;
@@ -218,10 +219,23 @@ __global__ __launch_bounds__(256) void k_kv_dequantize(KVCache c, KVSeqs s, uint
 // and through the hardware conversion straight into matrix operands; the
 // scale of a block multiplies the fp32 partial score (keys) or the weight
 // (values), never an element.
+//
+// Bound by memory: 4.5 bits an element (72 bytes a vector of 128), read once a
+// unit.  131071 tokens, 32 heads on 8: 34 us for 151 MB (4.5 TB/s) and 4.4 us
+// for the join; 64 sequences of up to 8192 tokens: 72 us for 302 MB.  About 240
+// vector instructions per 32 tokens and wave, half of what the same stream
+// would need with a 16-entry table looked up by byte permutes in place of the
+// hardware conversion.
 constexpr int kStep = 128;           // tokens per workgroup step, 32 a wave
 constexpr float kSlack = 8.0f;       // see the running maximum below
+// Units of at most this many steps are taken whole, without a join.  One
+// sequence, 32 heads on 8, whole and shared: 256 tokens 5.8 and 8.1 us, 512
+// tokens 7.8 and 8.2, 1024 tokens 11.9 and 8.3.
 constexpr int kSoloSteps = 4;
+// Workgroups per compute unit that share the steps, all resident at once: 2
+// (131071 tokens: 34 us; 3 make 39, 4 make 39, 6 make 44).
 constexpr int kWorkers = 2;
+// Rows up to which the join gives each a workgroup (see k_kv_join's launch).
 constexpr int64_t kWideRows = 1024;
 
 template <int D, int MT>
@@ -324,7 +338,7 @@ __device__ __forceinline__ bf16x8_t fp4_to_frag(uint32_t c) {
 }
 
 template <int D, int MT>
-__global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_kv_attention(KVCache c, KVSeqs s, const uint16_t* __restrict__ q,
+__global__ __launch_bounds__(256, 2) void k_kv_attention(KVCache c, KVSeqs s, const uint16_t* __restrict__ q,
                                                       int64_t q_stride, int Hq, float scale2,
                                                       uint16_t* __restrict__ out, float* __restrict__ ws, bool solo,
                                                       int fill) {
@@ -365,6 +379,7 @@ __global__ __launch_bounds__(256, MT <= 2 ? 2 : 1) void k_kv_attention(KVCache c
       continue;
     }
     const int ns = si.steps, share = solo ? 1 : ns;
+    if (lo < base) return;                         // only where overlapping offsets overflow the counts
     const int u = (lo - base) / share, s0 = lo - base - u * share, s1 = solo ? ns : min(ns, s0 + (hi - lo));
     const int rt = u / c.Hkv, h = u - rt * c.Hkv;
     // read by the scalar unit: nothing writes the table while the kernel runs
@@ -714,6 +729,7 @@ __global__ __launch_bounds__(256) void k_kv_join(KVCache c, KVSeqs s, int Hq, ui
   const int h = hq / G, row = (t - si.first) * G + (hq - h * G), rt = row / R, rr = row - rt * R;
   const int u0 = before + (rt * c.Hkv + h) * si.steps;
   const int w0 = u0 / per, w1 = (u0 + si.steps - 1) / per;
+  if (u0 < 0 || w1 >= workers) return;                       // only where overlapping offsets overflow the counts
   if (w0 == w1) return;                                      // one worker wrote the result
   const int grp = tid / LP, e = 4 * (tid % LP);
   Partial p{-INFINITY, 0.0f, {0.f, 0.f, 0.f, 0.f}};
@@ -775,7 +791,8 @@ hipError_t attend(const KVAttnPlan& pl, const KVCache& c, const KVSeqs& s, const
   const int64_t items = static_cast<int64_t>(s.T) * Hq;
   uint16_t* o = static_cast<uint16_t*>(out);
   const float* part = static_cast<const float*>(ws);
-  // 80 rows of 40 heads, 4 or 5 partial results each: 8.1 us with a workgroup a row, 5.5 with a wave
+  // 80 rows of 40 heads, 4 or 5 partial results each: 8.1 us with a workgroup a
+  // row, 4.8 with a wave; one row of 32 heads with 64 results: 4.4 with a workgroup
   if (items <= kWideRows)
     k_kv_join<D, MT, true><<<static_cast<unsigned>(items), 256, 0, stream>>>(c, s, Hq, o, part, static_cast<int>(pl.workers), fill);
   else
@@ -825,7 +842,10 @@ KVAttnPlan plan_kv_attention(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int3
   KVAttnPlan pl;
   const int64_t G = Hq / Hkv;
   const int64_t mean = B > 0 ? (T * G + B - 1) / B : G;      // rows per sequence and key head
-  pl.mt = mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
+  // 32 rows a unit where 16 do not hold a sequence's: 9 rows on 16 sequences of
+  // up to 4099 tokens, heads 32 on 8: 63.5 us, with 64 rows a unit (registers for
+  // one wave a SIMD only) 73.8
+  pl.mt = mean <= 16 ? 1 : 2;
   const int64_t units = (T * G / (16 * pl.mt) + B) * Hkv, steps = (tokens + kStep - 1) / kStep;
   pl.solo = steps <= kSoloSteps;
   pl.workers = pl.solo ? units : kWorkers * cus;
@@ -840,10 +860,8 @@ hipError_t launch_kv_attention(const KVAttnPlan& pl, const KVCache& c, const KVS
   if (c.D == D_ && pl.mt == MT_) return attend<D_, MT_>(pl, c, s, q, q_stride, Hq, scale, out, fill, ws, stream)
   NF4_ATTEND(64, 1);
   NF4_ATTEND(64, 2);
-  NF4_ATTEND(64, 4);
   NF4_ATTEND(128, 1);
   NF4_ATTEND(128, 2);
-  NF4_ATTEND(128, 4);
 #undef NF4_ATTEND
   return hipErrorInvalidValue;
 }
