@@ -116,6 +116,15 @@ __device__ __forceinline__ bf16x8_t pack8(const f32x16_t& p, int m) {
                                               pack_bf16x2(p[8 * m + 4], p[8 * m + 5]), pack_bf16x2(p[8 * m + 6], p[8 * m + 7])});
 }
 
+// What that rounding took from 8 values, itself rounded: the two together hold
+// 16 bits of each.
+__device__ __forceinline__ bf16x8_t rest8(const f32x16_t& p, int m, bf16x8_t high) {
+  f32x16_t r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = p[8 * m + i] - static_cast<float>(high[i]);
+  return pack8(r, 0);
+}
+
 // The tiles of 128 rows of all sequences, heaviest first: a sequence of t tiles
 // has one tile of each weight t, t-1, .. 1 (tiles of other rows that it works
 // through).  The z-th is found by bisection over the weight w, with
@@ -399,8 +408,9 @@ struct GradArgs {
 
 // grad_q: a wave keeps 32 query rows and streams keys and values.
 //   delta = dO . O, P = exp(scale S - lse), dS = P (dO V^T - delta), grad_q = scale dS K
-// 9195 rows in 6 sequences, 32 heads on 8 of 128: 226 us (3 products, 860
-// TFLOP/s; with S and dP formed together, one product each in turn, 242).
+// 9195 rows in 6 sequences, 32 heads on 8 of 128: 233 us (3 products, 840
+// TFLOP/s), 7 of them for what rounding took on the diagonal; with S and dP
+// formed together, one product each in turn, 16 more.
 template <int D>
 __global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, GradArgs g, uint16_t* __restrict__ gq, int bound) {
   constexpr int KS = D / 16, DT = D / 32;
@@ -486,6 +496,13 @@ __global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, GradArgs 
       const bf16x8_t pf = pack8(p.s, m);
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) acc[dt] = mfma(read_tr(kt, of, 2 * w + m, dt), pf, acc[dt]);
+      // on the diagonal, where a row's few score gradients cancel each other
+      // (they sum to zero), with what the rounding took
+      if constexpr (decltype(masked)::value) {
+        const bf16x8_t rf = rest8(p.s, m, pf);
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) acc[dt] = mfma(read_tr(kt, of, 2 * w + m, dt), rf, acc[dt]);
+      }
     }
   };
   auto step = [&](int j, auto masked) __attribute__((always_inline)) {
@@ -522,8 +539,9 @@ __global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, GradArgs 
 // rows and leaves them in LDS (bf16); then each multiplies the whole tile into
 // its half of the elements of grad_v and grad_k.  So the sums of a wave take 64
 // registers, not 128, and two waves fit a SIMD, one's exponentials under the
-// other's products.  9195 rows in 6 sequences, 32 heads on 8 of 128: 324 us
-// (4 products, 800 TFLOP/s); 4 waves that keep all sums, one a SIMD: 360 us.
+// other's products.  9195 rows in 6 sequences, 32 heads on 8 of 128: 343 us
+// (4 products, 760 TFLOP/s), 17 of them for what rounding took on the diagonal;
+// 4 waves that keep all sums, one a SIMD, took 360 without that.
 // Where the tiles alone leave compute units idle, the heads of a group are
 // split over `parts` workgroups, whose fp32 sums k_prompt_join adds in order.
 template <int D>
@@ -532,7 +550,7 @@ __global__ __launch_bounds__(512, 2) void k_prompt_bwd_kv(PromptArgs a, GradArgs
                                                           int bound) {
   constexpr int KS = D / 16, DT = D / 64;                       // 32-element tiles of a wave's half
   __shared__ __align__(1024) char lds[2][2][kTile * D * 2];     // [buffer][queries, output gradients]
-  __shared__ __align__(1024) char weights[2][kRows * kTile * 2];   // [P, dS][key][row of the tile]
+  __shared__ __align__(1024) char weights[3][kRows * kTile * 2];   // [P, dS, what rounding took from dS][key][row of the tile]
   __shared__ __align__(256) float stat[2][2][kTile];            // [buffer][lse, delta]
   const int x = blockIdx.x % (a.Hkv * parts), z = blockIdx.x / (a.Hkv * parts);
   const int hk = head_of(x / parts, a.Hkv), pt = x % parts;
@@ -609,10 +627,15 @@ __global__ __launch_bounds__(512, 2) void k_prompt_bwd_kv(PromptArgs a, GradArgs
       }
       const int at_q = wrow + (((4 * hf + b) ^ (l32 & 7)) << 4) + 8 * h;
       *reinterpret_cast<uint2*>(weights[0] + at_q) = make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
-      *reinterpret_cast<uint2*>(weights[1] + at_q) = make_uint2(pack_bf16x2(ds[0], ds[1]), pack_bf16x2(ds[2], ds[3]));
+      const uint2 high = make_uint2(pack_bf16x2(ds[0], ds[1]), pack_bf16x2(ds[2], ds[3]));
+      *reinterpret_cast<uint2*>(weights[1] + at_q) = high;
+      if constexpr (decltype(masked)::value)                    // as in grad_q's kernel
+        *reinterpret_cast<uint2*>(weights[2] + at_q) =
+            make_uint2(pack_bf16x2(ds[0] - __builtin_bit_cast(float, high.x << 16), ds[1] - __builtin_bit_cast(float, high.x & 0xFFFF0000u)),
+                       pack_bf16x2(ds[2] - __builtin_bit_cast(float, high.y << 16), ds[3] - __builtin_bit_cast(float, high.y & 0xFFFF0000u)));
     }
   };
-  auto gather = [&](int buf, int w) __attribute__((always_inline)) {
+  auto gather = [&](int buf, int w, auto masked) __attribute__((always_inline)) {
 #pragma unroll
     for (int m = 2 * w; m < 2 * w + 2; ++m) {
       const int at_q = wrow + (((2 * m + h) ^ (l32 & 7)) << 4);
@@ -623,7 +646,10 @@ __global__ __launch_bounds__(512, 2) void k_prompt_bwd_kv(PromptArgs a, GradArgs
         const char* q = lds[buf][0] + m * 1024 + dt * kSlice;
         const char* o = lds[buf][1] + m * 1024 + dt * kSlice;
         av[dt] = mfma(read_tr_at(o + tr[0], o + tr[1]), pf, av[dt]);
-        ak[dt] = mfma(read_tr_at(q + tr[0], q + tr[1]), sf, ak[dt]);
+        const bf16x8_t qf = read_tr_at(q + tr[0], q + tr[1]);
+        ak[dt] = mfma(qf, sf, ak[dt]);
+        if constexpr (decltype(masked)::value)
+          ak[dt] = mfma(qf, *reinterpret_cast<const bf16x8_t*>(weights[2] + at_q), ak[dt]);
       }
     }
   };
@@ -652,7 +678,7 @@ __global__ __launch_bounds__(512, 2) void k_prompt_bwd_kv(PromptArgs a, GradArgs
       share_lds();
 #pragma unroll
       for (int w = 0; w < 2; ++w)
-        if (!decltype(masked)::value || j * kTile + 32 * w + 31 >= w0) gather(buf, w);
+        if (!decltype(masked)::value || j * kTile + 32 * w + 31 >= w0) gather(buf, w, masked);
     }
     land();                                                     // the tiles are free again
   };
