@@ -78,14 +78,27 @@ hipError_t launch_prompt_bwd(const PromptArgs& a, const void* grad_out, int64_t 
 // wait for them themselves.  The LDS address is uniform, lane i lands 16 i
 // (4 i) bytes behind it.
 typedef __attribute__((address_space(3))) void lds_ptr_t;
+// ONCE: non-temporal, for data that no other workgroup reads.
+template <bool ONCE = false>
 __device__ __forceinline__ void copy16(uint32_t off, const char* base, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" :: "v"(off), "s"(base), "{m0}"(lds) : "memory");
+  if constexpr (ONCE)
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt" :: "v"(off), "s"(base), "{m0}"(lds) : "memory");
+  else
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" :: "v"(off), "s"(base), "{m0}"(lds) : "memory");
 }
+template <bool ONCE = false>
 __device__ __forceinline__ void copy16(const void* src, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(src), "{m0}"(lds) : "memory");
+  if constexpr (ONCE)
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" :: "v"(src), "{m0}"(lds) : "memory");
+  else
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" :: "v"(src), "{m0}"(lds) : "memory");
 }
+template <bool ONCE = false>
 __device__ __forceinline__ void copy4(const void* src, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" :: "v"(src), "{m0}"(lds) : "memory");
+  if constexpr (ONCE)
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off nt" :: "v"(src), "{m0}"(lds) : "memory");
+  else
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" :: "v"(src), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_ptr_t*)p));

@@ -221,8 +221,8 @@ __global__ __launch_bounds__(256) void k_kv_dequantize(KVCache c, KVSeqs s, uint
 // (values), never an element.
 //
 // Bound by memory: 4.5 bits an element (72 bytes a vector of 128), read once a
-// unit.  131071 tokens, 32 heads on 8: 34 us for 151 MB (4.5 TB/s) and 4.4 us
-// for the join; 64 sequences of up to 8192 tokens: 72 us for 302 MB.  About 240
+// unit.  131071 tokens, 32 heads on 8: 32 us for 151 MB (4.8 TB/s) and 4.4 us
+// for the join; 64 sequences of up to 8192 tokens: 71 us for 302 MB.  About 240
 // vector instructions per 32 tokens and wave, half of what the same stream
 // would need with a 16-entry table looked up by byte permutes in place of the
 // hardware conversion.
@@ -457,21 +457,24 @@ __global__ __launch_bounds__(256, 2) void k_kv_attention(KVCache c, KVSeqs s, co
       }
       at += kStep;
       KVTile<D>& t = ring[slot];
+      // one row tile a sequence: nobody else reads this (131071 tokens: 31.6 us, 33.8
+      // without the hint; several row tiles lose 1 to 6 % with it)
+      constexpr bool kOnce = MT == 1;
       const uint32_t l16 = 16 * lane;
       const int64_t mine = lane < 32 ? vec[0] : vec[1];
       if constexpr (D == 128) {                    // 16 tokens' patterns are 1024 bytes, their scales 128
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          copy16(l16, reinterpret_cast<const char*>(c.k_codes) + vec[w] * 64, lds_addr(t.k[w]));
-          copy16(l16, reinterpret_cast<const char*>(c.v_codes) + vec[w] * 64, lds_addr(t.v[w]));
+          copy16<kOnce>(l16, reinterpret_cast<const char*>(c.k_codes) + vec[w] * 64, lds_addr(t.k[w]));
+          copy16<kOnce>(l16, reinterpret_cast<const char*>(c.v_codes) + vec[w] * 64, lds_addr(t.v[w]));
         }
-        copy4(c.k_scale + mine * 2 + (lane & 31), lds_addr(t.ks));
-        copy4(c.v_scale + mine * 2 + (lane & 31), lds_addr(t.vs));
+        copy4<kOnce>(c.k_scale + mine * 2 + (lane & 31), lds_addr(t.ks));
+        copy4<kOnce>(c.v_scale + mine * 2 + (lane & 31), lds_addr(t.vs));
       } else {                                     // 512 and 64 bytes
-        copy16(c.k_codes + mine * 32 + 16 * (lane & 31), lds_addr(t.k));
-        copy16(c.v_codes + mine * 32 + 16 * (lane & 31), lds_addr(t.v));
+        copy16<kOnce>(c.k_codes + mine * 32 + 16 * (lane & 31), lds_addr(t.k));
+        copy16<kOnce>(c.v_codes + mine * 32 + 16 * (lane & 31), lds_addr(t.v));
         const int64_t other = (lane & 16) ? vec[1] : vec[0];
-        copy4((lane < 32 ? c.k_scale : c.v_scale) + other + (lane & 15), lds_addr(t.ks));
+        copy4<kOnce>((lane < 32 ? c.k_scale : c.v_scale) + other + (lane & 15), lds_addr(t.ks));
       }
     };
 
