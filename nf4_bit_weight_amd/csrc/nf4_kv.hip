@@ -233,7 +233,7 @@ constexpr float kSlack = 8.0f;       // see the running maximum below
 // tokens 7.8 and 8.2, 1024 tokens 11.9 and 8.3.
 constexpr int kSoloSteps = 4;
 // Workgroups per compute unit that share the steps, all resident at once: 2
-// (131071 tokens: 34 us; 3 make 39, 4 make 39, 6 make 44).
+// (131071 tokens, before non-temporal reads: 34 us; 3 make 39, 4 make 39, 6 make 44).
 constexpr int kWorkers = 2;
 // Rows up to which the join gives each a workgroup (see k_kv_join's launch).
 constexpr int64_t kWideRows = 1024;

@@ -238,7 +238,7 @@ __device__ __forceinline__ int head_of(int x, int heads) { return heads % 8 == 0
 // One workgroup: 128 query rows of one head, streaming keys and values.  Bound
 // by the matrix and vector units together (a 64-key tile is 1024 cycles of
 // products and about 900 of exponentials and sums a wave, two waves a SIMD):
-// 8192 rows, 32 heads on 8 of 128: 516 us, 1070 TFLOP/s, where this card's
+// 8192 rows, 32 heads on 8 of 128: 501 us, 1097 TFLOP/s, where this card's
 // library product of 8192 cubed reaches 1240.  The running maximum moves only when a score passes it by 2^kSlack, so the
 // rescaling of the sums is rare; weights are then at most 2^kSlack, which
 // costs bf16 and fp32 nothing.
