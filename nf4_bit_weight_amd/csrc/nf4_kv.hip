@@ -851,7 +851,7 @@ KVAttnPlan plan_kv_attention(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int3
   pl.mt = mean <= 16 ? 1 : 2;
   const int64_t units = (T * G / (16 * pl.mt) + B) * Hkv, steps = (tokens + kStep - 1) / kStep;
   pl.solo = steps <= kSoloSteps;
-  pl.workers = pl.solo ? units : kWorkers * cus;
+  pl.workers = pl.solo ? (units > 0 ? units : 1) : kWorkers * cus;   // one even without sequences: rows outside are filled
   pl.steps = steps > 0 && units > INT64_MAX / steps ? INT64_MAX : units * (steps > 0 ? steps : 1);
   pl.ws_bytes = pl.solo ? 0 : 2 * static_cast<size_t>(pl.workers) * (16 * pl.mt * (D + 2)) * sizeof(float);
   return pl;

@@ -475,3 +475,23 @@ def test_refusals():
     with pytest.raises(RuntimeError):                                                  # rows not 16-byte aligned
         y = torch.empty(3 * 128 + 1, dtype=torch.bfloat16, device=DEV)[1:].view(3, 2, 64)
         nf4_kv_attention(y, cache, lens, table, offsets=off)
+
+
+@pytest.mark.parametrize("width", [0, 2, 100])
+def test_no_sequences(width):
+    """Rows of a call without sequences are all padding: zeros in new results,
+    left alone in given ones."""
+    T, Hq, D = 5, 2, 64
+    q, k = R.normal(7, T, Hq, D).to(DEV), R.normal(8, T, Hq, D).to(DEV)
+    cache = nf4_kv_cache(3, Hq, 16, D, device=DEV)
+    ln, off, table = i32([]), i32([0]), torch.zeros((0, width), dtype=torch.int32, device=DEV)
+    assert not nf4_kv_attention(q, cache, ln, table, off).any()
+    given = torch.full((T, Hq, D), 3.0, dtype=torch.bfloat16, device=DEV)
+    nf4_kv_attention(q, cache, ln, table, off, out=given)
+    assert (given == 3.0).all()
+    qo, ko = nf4_kv_append(cache, k, k, ln, table, off, q=q, return_k=True)
+    assert not qo.any() and not ko.any()
+    assert not any(x.any() for x in nf4_kv_dequantize(cache, ln, table, off, rows=T))
+    for n in (0, T):                                          # an empty first sequence, and none of the cache's pages
+        empty = nf4_kv_attention(q, cache, i32([n]), torch.full((1, width), 9, dtype=torch.int32, device=DEV), i32([0, n]))
+        assert not empty.any()
