@@ -17,7 +17,11 @@
  * *_stride is the distance between rows in elements (a multiple of 8, at most
  * 2^24; the heads of one row are contiguous), so slices of a joint projection are taken
  * as they are.  All row pointers are 16-byte aligned.  Written tensors are
- * contiguous.
+ * contiguous and overlap nothing that the call reads.  Calls are refused
+ * (NF4_ERR_UNSUPPORTED) above 1024 query heads, 2^31 - 1 (row, query head) pairs
+ * or 2^32 - 1 threads in a launch: 2^26 rows appended, 2^24 groups of 4 (row,
+ * query head) pairs joined, and for prompts 2^24 (2^23 backward) tiles of 128
+ * rows times query heads, each sequence counting one tile more.
  *
  * Sequences.  offsets int32 [B + 1] as in the grouped calls of nf4.h: rows
  * offsets[b] .. offsets[b+1]-1 belong to sequence b, non-decreasing, empty
@@ -71,7 +75,6 @@ extern "C" {
  *              bits and rounded once to bf16; the cache keeps the rounded keys.
  *   q, q_out   NULL together: no queries.  q_out bf16 [T, Hq, D].
  *   k_out      NULL, or bf16 [T, Hkv, D]: the rotated keys.
- * q_out and k_out may not overlap the inputs.
  */
 int nf4_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                   const void* v, int64_t v_stride, int64_t T, int32_t Hq,
@@ -135,7 +138,8 @@ int nf4_prompt_attention_fwd(const void* q, int64_t q_stride, const void* k, int
  * [T, Hkv, D] (summed over the query heads that share a key head) from
  * grad_out bf16 (row stride grad_stride), the inputs, and out, out_rest and lse of
  * the forward call.  Without out_rest (NULL) grad_out . out is taken from the
- * rounded output, which adds its rounding to grad_q and grad_k.
+ * rounded output, which adds its rounding to grad_q and grad_k.  A NaN or an
+ * infinity in a row may reach every gradient of its sequence, and of no other.
  *   ws  nf4_prompt_attention_bwd_workspace(...) bytes, 16-byte aligned
  */
 int nf4_prompt_attention_bwd(const void* grad_out, int64_t grad_stride,

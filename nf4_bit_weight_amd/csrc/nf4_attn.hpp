@@ -62,6 +62,7 @@ struct KVAttnPlan {
   size_t ws_bytes;
 };
 KVAttnPlan plan_kv_attention(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int64_t tokens, int cus);
+int64_t kv_join_groups(int64_t T, int32_t Hq);                 // workgroups of the join
 hipError_t launch_kv_attention(const KVAttnPlan& pl, const KVCache& c, const KVSeqs& s, const void* q,
                                int64_t q_stride, int32_t Hq, float scale, void* out, int fill, void* ws,
                                hipStream_t stream);

@@ -10,8 +10,14 @@
 namespace nf4 {
 namespace {
 
+// Workgroups of the prompt's kernels: one per (128 rows or sequence, head).
+int64_t prompt_groups(int64_t T, int32_t B, int32_t heads) { return (T / 128 + B + 1) * heads; }
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int to_status(hipError_t e) { return e == hipSuccess ? NF4_OK : NF4_ERR_HIP; }
+
+// A launch takes fewer than 2^32 threads.
+bool launchable(int64_t workgroups, int64_t threads) { return workgroups <= UINT32_MAX / threads; }
 
 // Sizes of T rows in B sequences with Hq query heads on Hkv key heads of D.
 int check_heads(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
@@ -19,8 +25,7 @@ int check_heads(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
   if (Hq % Hkv) return NF4_ERR_SHAPE;
   if (D != 64 && D != 128) return NF4_ERR_UNSUPPORTED;
   if (T > INT32_MAX / 4 || B > INT32_MAX / 4 || Hq > 1024) return NF4_ERR_UNSUPPORTED;
-  // one workgroup per (128 rows or sequence, head)
-  if ((T / 128 + B + 1) * Hq > INT32_MAX) return NF4_ERR_UNSUPPORTED;
+  if (T * Hq > INT32_MAX) return NF4_ERR_UNSUPPORTED;        // (row, head) pairs are counted in 32 bits
   return NF4_OK;
 }
 
@@ -78,6 +83,7 @@ int nf4_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stri
   if (T > 0 && q && !q_out) return NF4_ERR_NULL;
   if (!aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(inv_freq, 4)) return NF4_ERR_ALIGN;
   if (T == 0) return NF4_OK;
+  if (!launchable((T + 3) / 4, 256)) return NF4_ERR_UNSUPPORTED;
   const KVCache c{k_codes, k_scale, v_codes, v_scale, P, page, Hkv, D};
   const KVSeqs s{offsets, lengths, page_table, B, width, static_cast<int32_t>(T)};
   const AppendArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
@@ -99,6 +105,7 @@ int nf4_kv_dequantize(int64_t T, const int32_t* offsets, const int32_t* lengths,
   if (T > 0 && (!k_out || !v_out)) return NF4_ERR_NULL;
   if (!aligned(k_out, 16) || !aligned(v_out, 16)) return NF4_ERR_ALIGN;
   if (T == 0) return NF4_OK;
+  if (!launchable((T + 3) / 4, 256)) return NF4_ERR_UNSUPPORTED;
   const KVCache c{const_cast<uint8_t*>(k_codes), const_cast<float*>(k_scale), const_cast<uint8_t*>(v_codes),
                   const_cast<float*>(v_scale), P, page, Hkv, D};
   const KVSeqs s{offsets, lengths, page_table, B, width, static_cast<int32_t>(T)};
@@ -131,7 +138,8 @@ int nf4_kv_attention(const void* q, int64_t q_stride, int64_t T, int32_t Hq, con
   if (P == 0) width = 0;                                     // no pages: no key is seen (and no workspace is needed)
   const KVAttnPlan pl = plan_kv_attention(T, B, Hq, Hkv, D, static_cast<int64_t>(width) * page, device_cu_count());
   // units and their steps of 128 tokens are counted in 32 bits
-  if (pl.steps > INT32_MAX / 2 || pl.workers > INT32_MAX / 2) return NF4_ERR_UNSUPPORTED;
+  if (pl.steps > INT32_MAX / 2 || !launchable(pl.workers, 256)) return NF4_ERR_UNSUPPORTED;
+  if (!pl.solo && !launchable(kv_join_groups(T, Hq), 256)) return NF4_ERR_UNSUPPORTED;
   if (pl.ws_bytes > 0 && (!ws || ws_bytes < pl.ws_bytes)) return NF4_ERR_WORKSPACE;
   if (pl.ws_bytes > 0 && !aligned(ws, 16)) return NF4_ERR_ALIGN;
   const KVCache c{const_cast<uint8_t*>(k_codes), const_cast<float*>(k_scale), const_cast<uint8_t*>(v_codes),
@@ -156,6 +164,7 @@ int nf4_prompt_attention_fwd(const void* q, int64_t q_stride, const void* k, int
   if (!offsets || (T > 0 && !out)) return NF4_ERR_NULL;
   if (!aligned(out, 16) || !aligned(out_rest, 16) || !aligned(lse, 4) || !aligned(offsets, 4)) return NF4_ERR_ALIGN;
   if (T == 0) return NF4_OK;
+  if (!launchable(prompt_groups(T, B, Hq), 256)) return NF4_ERR_UNSUPPORTED;
   const PromptArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                      q_stride, k_stride, v_stride, offsets, static_cast<int32_t>(T), B, Hq, Hkv, D, scale,
                      fill_outside != 0};
@@ -186,6 +195,8 @@ int nf4_prompt_attention_bwd(const void* grad_out, int64_t grad_stride, const vo
       !aligned(offsets, 4))
     return NF4_ERR_ALIGN;
   if (T == 0) return NF4_OK;
+  // grad_k's workgroups are of 512 threads and split the heads of a group at most to one each
+  if (!launchable(prompt_groups(T, B, Hq), 512)) return NF4_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < prompt_bwd_ws_bytes(T, B, Hq, Hkv, D)) return NF4_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return NF4_ERR_ALIGN;
   const PromptArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),

@@ -791,15 +791,15 @@ hipError_t attend(const KVAttnPlan& pl, const KVCache& c, const KVSeqs& s, const
       pl.solo, fill);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.solo) return e;
-  const int64_t items = static_cast<int64_t>(s.T) * Hq;
+  const unsigned groups = static_cast<unsigned>(kv_join_groups(s.T, Hq));
   uint16_t* o = static_cast<uint16_t*>(out);
   const float* part = static_cast<const float*>(ws);
   // 80 rows of 40 heads, 4 or 5 partial results each: 8.1 us with a workgroup a
   // row, 4.8 with a wave; one row of 32 heads with 64 results: 4.4 with a workgroup
-  if (items <= kWideRows)
-    k_kv_join<D, MT, true><<<static_cast<unsigned>(items), 256, 0, stream>>>(c, s, Hq, o, part, static_cast<int>(pl.workers), fill);
+  if (static_cast<int64_t>(s.T) * Hq <= kWideRows)
+    k_kv_join<D, MT, true><<<groups, 256, 0, stream>>>(c, s, Hq, o, part, static_cast<int>(pl.workers), fill);
   else
-    k_kv_join<D, MT, false><<<static_cast<unsigned>((items + 3) / 4), 256, 0, stream>>>(c, s, Hq, o, part, static_cast<int>(pl.workers), fill);
+    k_kv_join<D, MT, false><<<groups, 256, 0, stream>>>(c, s, Hq, o, part, static_cast<int>(pl.workers), fill);
   return hipGetLastError();
 }
 
@@ -840,6 +840,8 @@ hipError_t launch_kv_dequantize(const KVCache& c, const KVSeqs& s, void* k_out, 
 #undef NF4_DEQUANTIZE
   return hipGetLastError();
 }
+
+int64_t kv_join_groups(int64_t T, int32_t Hq) { return T * Hq <= kWideRows ? T * Hq : (T * Hq + 3) / 4; }
 
 KVAttnPlan plan_kv_attention(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int64_t tokens, int cus) {
   KVAttnPlan pl;

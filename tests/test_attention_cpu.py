@@ -163,3 +163,23 @@ def test_reference_encoding_round_trip():
     top = y.double().unflatten(-1, (-1, 64)).abs().amax(-1, keepdim=True)
     # half of the widest step, and the fp32 rounding of the scale
     assert ((R.decode(c, s) - y.double()).unflatten(-1, (-1, 64)).abs() <= top * (1 / 6 + 2.0 ** -20)).all()
+
+
+def test_refuses_what_a_launch_cannot_take(lib):
+    """Launches of 2^32 threads and (row, head) pairs beyond 32 bits are refused
+    before anything is enqueued."""
+    no = L.NF4_ERR_UNSUPPORTED
+    assert append(lib, T=1 << 26) == no
+    assert lib.nf4_kv_dequantize(1 << 26, A, A, 1, A, 1, A, A, A, A, 1, 16, 2, 64, A, A, 1, None) == no
+    assert attention(lib, T=1 << 23, B=1 << 23, off=None, Hq=1024, Hkv=1) == no            # 2^33 pairs
+    assert attention(lib, T=1 << 25, Hq=16, Hkv=16, width=4) == no                         # 2^24 units of 32 rows, whole
+    assert attention(lib, T=1 << 22, Hq=16, Hkv=2, width=100, wsb=1 << 40) == no           # 2^24 groups of 4 in the join
+    x = (A, 1024, A, 1024, A, 1024)
+
+    def fwd(T, B, H):
+        return lib.nf4_prompt_attention_fwd(*x, T, A, B, H, H, 64, 0.125, A, None, A, 1, None)
+
+    def bwd(T, B, H):
+        return lib.nf4_prompt_attention_bwd(A, 1024, *x, A, None, A, T, A, B, H, H, 64, 0.125, A, A, A, 1, A, 1 << 50, None)
+    assert fwd(128, (1 << 20) - 1, 16) == no and bwd(128, (1 << 19) - 1, 16) == no
+    assert fwd(1 << 28, 1, 16) == no and bwd(1 << 28, 1, 16) == no
