@@ -106,6 +106,12 @@ def nf4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offs
     (int32 [B + 1]) cut q [T, Hq, D] and k, v [T, Hkv, D] into; differentiable in
     q, k and v, once.  The kernels compute in bf16 with fp32 accumulation; the
     output and the gradients come back in the dtypes that the caller passed in.
-    Rows outside every sequence are zeros in both.  (The autograd node is in
+    Rows outside every sequence are zeros in both.
+
+    Forward and backward can be captured into a graph together.  No eager graph
+    of the same leaves may live then: its gradient accumulators belong to the
+    eager stream, and autograd would draw that stream into the capture.  Leaves
+    that are q, k or v themselves are checked; for leaves further up, drop the
+    eager results before the capture.  (The autograd node is in
     csrc/nf4_torch.cpp and saves tensors only, through save_for_backward.)"""
     return attention._call("prompt_attention", q, k, v, offsets, scale)

@@ -14,13 +14,17 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/variable.h>
 
 #include <cmath>
+#include <initializer_list>
 #include <optional>
 #include <sstream>
 #include <stdexcept>
 #include <string>
+#include <utility>
 
 #include "../../include/nf4_attn.h"
 
@@ -410,6 +414,23 @@ struct PromptAttention : torch::autograd::Function<PromptAttention> {
   }
 };
 
+// While a graph is being captured, the gradients of leaves go through their
+// accumulators.  One that a living eager graph made belongs to the eager stream,
+// and autograd would make that stream wait inside the capture, which ends it,
+// and the process with it.  So such a leaf is refused here, in the forward call.
+void check_capture(std::initializer_list<std::pair<const char*, const Tensor*>> inputs, const c10::Device& dev) {
+  const auto now = c10::hip::getCurrentHIPStream(dev.index());
+  hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(now.stream(), &status) != hipSuccess || status != hipStreamCaptureStatusActive) return;
+  for (const auto& [name, t] : inputs) {
+    if (!t->requires_grad() || !t->is_leaf()) continue;
+    const auto acc = torch::autograd::impl::try_get_grad_accumulator(*t);
+    const auto stream = acc ? acc->stream() : std::nullopt;
+    if (stream && stream->id() != now.id())
+      refuse(name, " is captured while an eager graph of the same leaf lives: drop that graph first, or pass a detached leaf");
+  }
+}
+
 // (q, k, v, offsets, scale): any floating dtype and layout, differentiable
 PyObject* prompt_attention(PyObject* const* a) {
   const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &offsets = tensor(a[3], "offsets");
@@ -418,6 +439,7 @@ PyObject* prompt_attention(PyObject* const* a) {
   if (q.dim() != 3) refuse("q must be [T, Hq, D] with D 64 or 128, got ", q.sizes());
   const Scale given_scale = scale_arg(a[4]);
   if (at::GradMode::is_enabled() && (q.requires_grad() || k.requires_grad() || v.requires_grad())) {
+    check_capture({{"q", &q}, {"k", &k}, {"v", &v}}, q.device());
     const double scale = given_scale ? *given_scale : 1.0 / std::sqrt(static_cast<double>(q.size(2)));
     return wrap(PromptAttention::apply(q, k, v, offsets, scale));
   }

@@ -328,3 +328,53 @@ def test_path_counts_and_refusals():
         nf4_prompt_attention_bwd(x, x, x, x, out, rest, lse[:1], off)
     with pytest.raises(RuntimeError):
         nf4_prompt_attention_bwd(x, x, x, x, out, rest, lse, off, ws=torch.empty(16, dtype=torch.uint8, device=DEV))
+
+
+def leaves():
+    _, q, k, v = inputs([100], 4, 2, 64, seed=5)
+    return [x.to(DEV).contiguous().requires_grad_() for x in (q, k, v)]
+
+
+def test_captured_step_of_leaves():
+    """Forward and backward through autograd, captured and replayed on changed
+    inputs."""
+    xs, off = leaves(), torch.tensor([0, 37, 100], dtype=torch.int32, device=DEV)
+    gy = R.normal(93, 100, 4, 64).to(DEV)
+
+    def step(xs):
+        y = nf4_prompt_attention(*xs, off)
+        return (y.detach(), *torch.autograd.grad(y, xs, gy))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(xs)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(xs)
+    for seed in range(3):
+        with torch.no_grad():
+            for i, x in enumerate(xs):
+                x.copy_(R.normal(200 + 3 * seed + i, *x.shape))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step([x.detach().requires_grad_() for x in xs])
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), seed
+
+
+def test_capture_refuses_leaves_of_a_living_eager_graph():
+    xs, off = leaves(), torch.tensor([0, 100], dtype=torch.int32, device=DEV)
+    alive = nf4_prompt_attention(*xs, off)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="eager graph"):
+            nf4_prompt_attention(*xs, off)
+        with torch.no_grad():
+            out = nf4_prompt_attention(*xs, off)               # no backward pass, no accumulators
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, alive.detach())
+    grads = torch.autograd.grad(alive, xs, torch.ones_like(alive))
+    assert all(g.isfinite().all() for g in grads)
