@@ -132,6 +132,13 @@ __device__ __forceinline__ f32x2_t swap32(float x) {
   asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(x), "+v"(y));
   return f32x2_t{x, y};
 }
+// Two dwords of row chunk b and two of chunk b + 1 (8 elements each, their
+// first half in the lower 32 lanes, the other in the upper) become four dwords
+// of chunk b in the lower lanes and of chunk b + 1 in the upper.
+__device__ __forceinline__ void halves(uint32_t (&x)[4]) {
+  asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %2\n\tv_permlane32_swap_b32 %1, %3"
+               : "+v"(x[0]), "+v"(x[1]), "+v"(x[2]), "+v"(x[3]));
+}
 __device__ __forceinline__ f32x2_t swap16(float x) {
   float y = x;
   asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(x), "+v"(y));

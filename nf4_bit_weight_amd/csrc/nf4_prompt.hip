@@ -230,6 +230,33 @@ struct TileShare {
   }
 };
 
+// The results of one wave on their way out, 32 rows of D elements through its
+// own part of LDS: a lane holds a row's elements in pieces of 4, and 32 rows with
+// a piece each keep the memory busy several times as long as 4 whole rows.
+template <int D>
+struct RowChunks {
+  static constexpr int kChunks = D / 8;                         // of 16 bytes a row
+  char* stage;
+  __device__ __forceinline__ explicit RowChunks(char* s) : stage(s) {}
+  // elements 32 dt + 16 p .. +15 of row (lane & 31): 4 h .. +3 of both halves of 8, two a dword
+  __device__ __forceinline__ void put(int dt, int p, uint32_t (&x)[4]) const {
+    const int lane = threadIdx.x & 63, row = lane & 31;
+    halves(x);                                                  // now 8 neighbouring elements
+    *reinterpret_cast<u32x4_t*>(stage + row * D * 2 + (((4 * dt + 2 * p + (lane >> 5)) ^ (row & (kChunks - 1))) << 4)) =
+        u32x4_t{x[0], x[1], x[2], x[3]};
+  }
+  __device__ __forceinline__ void store(uint16_t* dst, int64_t stride, int rows) const {
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < kChunks / 2; ++i) {
+      const int at = 64 * i + static_cast<int>(threadIdx.x & 63), row = at / kChunks, ch = at % kChunks;
+      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(stage + row * D * 2 + ((ch ^ (row & (kChunks - 1))) << 4));
+      if (row < rows) *reinterpret_cast<u32x4_t*>(dst + row * stride + 8 * ch) = x;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+};
+
 // Heads of one key head next to each other in one XCD's queue (workgroups go
 // round the 8 XCDs in order), so that they share its L2.
 __device__ __forceinline__ int head_of(int x, int heads) { return heads % 8 == 0 ? (x % 8) * (heads / 8) + x / 8 : x; }
@@ -378,24 +405,40 @@ __global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* _
     if (j + 1 < tiles) scores(j + 1, s0);
   }
   const float total = half_sum(sum[0] + sum[1]);
-  if (qi >= at.n) return;
   const float f = 1.0f / total;                                 // every row sees itself
-  const int64_t t = static_cast<int64_t>(at.first) + qi;
-  if (lse && h == 0) lse[static_cast<int64_t>(hq) * a.T + t] = (__builtin_amdgcn_logf(total) + ref) * kLn2;
-  const int64_t dst = (t * a.Hq + hq) * D + 4 * h;
+  if (lse && h == 0 && qi < at.n)
+    lse[static_cast<int64_t>(hq) * a.T + at.first + qi] = (__builtin_amdgcn_logf(total) + ref) * kLn2;
+  // the keys are read to their end: their buffers take the results
+  char* const stage = lds[wave >> 1][0] + (wave & 1) * 32 * D * 2;
+  u32x4_t left[DT][2];
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const float y[4] = {acc[dt][4 * b] * f, acc[dt][4 * b + 1] * f, acc[dt][4 * b + 2] * f, acc[dt][4 * b + 3] * f};
-      const uint2 o = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
-      *reinterpret_cast<uint2*>(out + dst + 32 * dt + 8 * b) = o;
-      // what the rounding took, for the backward pass
-      if (rest)
-        *reinterpret_cast<uint2*>(rest + dst + 32 * dt + 8 * b) =
-            make_uint2(pack_bf16x2(y[0] - __builtin_bit_cast(float, o.x << 16), y[1] - __builtin_bit_cast(float, o.x & 0xFFFF0000u)),
-                       pack_bf16x2(y[2] - __builtin_bit_cast(float, o.y << 16), y[3] - __builtin_bit_cast(float, o.y & 0xFFFF0000u)));
+    for (int p = 0; p < 2; ++p) {
+      const RowChunks<D> to(stage);
+      uint32_t o[4], r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float y0 = acc[dt][8 * p + 2 * i] * f, y1 = acc[dt][8 * p + 2 * i + 1] * f;
+        o[i] = pack_bf16x2(y0, y1);
+        // what the rounding took, for the backward pass
+        r[i] = pack_bf16x2(y0 - __builtin_bit_cast(float, o[i] << 16), y1 - __builtin_bit_cast(float, o[i] & 0xFFFF0000u));
+      }
+      to.put(dt, p, o);
+      left[dt][p] = u32x4_t{r[0], r[1], r[2], r[3]};
     }
+  const int64_t dst = (static_cast<int64_t>(at.first + w0) * a.Hq + hq) * D;
+  RowChunks<D>(stage).store(out + dst, static_cast<int64_t>(a.Hq) * D, at.n - w0);
+  if (rest) {
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        uint32_t r[4] = {left[dt][p][0], left[dt][p][1], left[dt][p][2], left[dt][p][3]};
+        RowChunks<D>(stage).put(dt, p, r);
+      }
+    RowChunks<D>(stage).store(rest + dst, static_cast<int64_t>(a.Hq) * D, at.n - w0);
+  }
 }
 
 // ---- backward --------------------------------------------------------------------
