@@ -245,6 +245,20 @@ struct RowChunks {
     *reinterpret_cast<u32x4_t*>(stage + row * D * 2 + (((4 * dt + 2 * p + (lane >> 5)) ^ (row & (kChunks - 1))) << 4)) =
         u32x4_t{x[0], x[1], x[2], x[3]};
   }
+  // and the other way: rows w0 .. w0+31 of a sequence of n (the last one again behind its end)
+  __device__ __forceinline__ void fetch(const uint16_t* seq, int64_t stride, int w0, int n) const {
+    const int top = min(w0, n - 1);
+    const char* base = reinterpret_cast<const char*>(seq + top * stride);
+#pragma unroll
+    for (int i = 0; i < kChunks / 2; ++i) {
+      const int at = 64 * i + static_cast<int>(threadIdx.x & 63), row = at / kChunks, ch = (at % kChunks) ^ (row & (kChunks - 1));
+      copy16(static_cast<uint32_t>(min(row, n - 1 - top)) * static_cast<uint32_t>(2 * stride) + 16 * ch, base, lds_addr(stage + 1024 * i));
+    }
+  }
+  __device__ __forceinline__ bf16x8_t read(int ks) const {      // elements 16 ks + 8 (lane >> 5) .. +7 of row (lane & 31)
+    const int lane = threadIdx.x & 63, row = lane & 31;
+    return *reinterpret_cast<const bf16x8_t*>(stage + row * D * 2 + (((2 * ks + (lane >> 5)) ^ (row & (kChunks - 1))) << 4));
+  }
   __device__ __forceinline__ void store(uint16_t* dst, int64_t stride, int rows) const {
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -293,12 +307,10 @@ __global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* _
   const int tiles = (min(at.n, q0 + kRows) + kTile - 1) / kTile;
   const int whole = q0 / kTile;                                 // tiles that every row sees whole: an even number
   ck(kb, 0, at.n, lds[0][0]);
+  // queries come through the second buffers, as whole rows too
+  const RowChunks<D> qs(lds[1][wave >> 1] + (wave & 1) * 32 * D * 2);
+  qs.fetch(a.q + at.first * a.q_stride + hq * D, a.q_stride, w0, at.n);
   bf16x8_t qf[KS];
-  {
-    const uint16_t* src = a.q + (static_cast<int64_t>(at.first) + min(qi, at.n - 1)) * a.q_stride + hq * D + 8 * h;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) qf[ks] = *reinterpret_cast<const bf16x8_t*>(src + 16 * ks);
-  }
   f32x16_t acc[DT];
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt) acc[dt] = zero16();
@@ -359,8 +371,11 @@ __global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* _
   f32x16_t s0[2], s1[2];
   if (threadIdx.x < 2) odd[threadIdx.x] = 0;
   land();
-  if (1 < tiles) ck(kb, kTile, at.n, lds[1][0]);
   cv(vb, 0, at.n, lds[0][1]);
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) qf[ks] = qs.read(ks);
+  share_lds();
+  if (1 < tiles) ck(kb, kTile, at.n, lds[1][0]);
   scores(0, s0);
   for (int j = 0; j < whole; j += 2) {
     advance(j);
