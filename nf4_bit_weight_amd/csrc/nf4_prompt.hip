@@ -578,15 +578,18 @@ __global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, GradArgs 
   };
   for (int j = 0; j < whole; ++j) step(j, std::false_type{});
   for (int j = whole; j < tiles; ++j) step(j, std::true_type{});  // at most two, on the diagonal
-  if (qi >= at.n) return;
-  uint16_t* dst = gq + (t * a.Hq + hq) * D + 4 * h;
+  // out through the buffers that the last tile does not use
+  const RowChunks<D> to(lds[tiles & 1][wave >> 1] + (wave & 1) * 32 * D * 2);
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-      *reinterpret_cast<uint2*>(dst + 32 * dt + 8 * b) =
-          make_uint2(pack_bf16x2(acc[dt][4 * b] * a.scale, acc[dt][4 * b + 1] * a.scale),
-                     pack_bf16x2(acc[dt][4 * b + 2] * a.scale, acc[dt][4 * b + 3] * a.scale));
+    for (int p = 0; p < 2; ++p) {
+      uint32_t x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = pack_bf16x2(acc[dt][8 * p + 2 * i] * a.scale, acc[dt][8 * p + 2 * i + 1] * a.scale);
+      to.put(dt, p, x);
+    }
+  to.store(gq + (static_cast<int64_t>(at.first + w0) * a.Hq + hq) * D, static_cast<int64_t>(a.Hq) * D, at.n - w0);
 }
 
 // grad_k and grad_v: a workgroup of 8 waves keeps 128 keys with their values
@@ -742,9 +745,9 @@ __global__ __launch_bounds__(512, 2) void k_prompt_bwd_kv(PromptArgs a, GradArgs
   };
   sweep(front + edge, 0, std::true_type{});
   sweep(inner, front, std::false_type{});
-  if (ki >= at.n) return;
-  const int64_t at_out = (t * a.Hkv + hk) * D + 32 * DT * hf + 4 * h;
   if (parts > 1) {
+    if (ki >= at.n) return;
+    const int64_t at_out = (t * a.Hkv + hk) * D + 32 * DT * hf + 4 * h;
     const int64_t set = static_cast<int64_t>(a.T) * a.Hkv * D;
     float* dst = part + 2 * pt * set + at_out;
 #pragma unroll
@@ -756,16 +759,22 @@ __global__ __launch_bounds__(512, 2) void k_prompt_bwd_kv(PromptArgs a, GradArgs
       }
     return;
   }
+  const RowChunks<D / 2> to(lds[0][0] + wave * 32 * D);           // a wave's half rows
+  const int64_t dst = (static_cast<int64_t>(at.first + w0) * a.Hkv + hk) * D + 32 * DT * hf;
+  auto leave = [&](const f32x16_t (&x)[DT], float f, uint16_t* grad) __attribute__((always_inline)) {
 #pragma unroll
-  for (int dt = 0; dt < DT; ++dt)
+    for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      *reinterpret_cast<uint2*>(gk + at_out + 32 * dt + 8 * b) =
-          make_uint2(pack_bf16x2(ak[dt][4 * b] * a.scale, ak[dt][4 * b + 1] * a.scale),
-                     pack_bf16x2(ak[dt][4 * b + 2] * a.scale, ak[dt][4 * b + 3] * a.scale));
-      *reinterpret_cast<uint2*>(gv + at_out + 32 * dt + 8 * b) =
-          make_uint2(pack_bf16x2(av[dt][4 * b], av[dt][4 * b + 1]), pack_bf16x2(av[dt][4 * b + 2], av[dt][4 * b + 3]));
-    }
+      for (int p = 0; p < 2; ++p) {
+        uint32_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = pack_bf16x2(x[dt][8 * p + 2 * i] * f, x[dt][8 * p + 2 * i + 1] * f);
+        to.put(dt, p, y);
+      }
+    to.store(grad + dst, static_cast<int64_t>(a.Hkv) * D, at.n - w0);
+  };
+  leave(ak, a.scale, gk);
+  leave(av, 1.0f, gv);
 }
 
 // Adds the parts of grad_k and grad_v in order; rows outside every sequence
