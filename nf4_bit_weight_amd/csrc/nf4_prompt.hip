@@ -461,7 +461,7 @@ struct GradArgs {
   const uint16_t *go, *out, *rest;
   int64_t go_stride;
   const float* lse;
-  float* stat;              // [2][Hq][T]: lse log2(e) and delta, grad_q's kernel to grad_k's
+  float* stat;              // [2][Hq][T]: lse log2(e) and -delta, grad_q's kernel to grad_k's
 };
 
 // grad_q: a wave keeps 32 query rows and streams keys and values.
@@ -522,7 +522,7 @@ __global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, GradArgs 
   const float ls = g.lse[st] * kLog2e;
   if (qi < at.n && h == 0) {
     g.stat[st] = ls;
-    g.stat[static_cast<int64_t>(a.Hq) * a.T + st] = delta;
+    g.stat[static_cast<int64_t>(a.Hq) * a.T + st] = -delta;
   }
   f32x16_t acc[DT];
 #pragma unroll
@@ -612,7 +612,7 @@ __global__ __launch_bounds__(512, 2) void k_prompt_bwd_kv(PromptArgs a, GradArgs
   constexpr int KS = D / 16, DT = D / 64;                       // 32-element tiles of a wave's half
   __shared__ __align__(1024) char lds[2][2][kTile * D * 2];     // [buffer][queries, output gradients]
   __shared__ __align__(1024) char weights[3][kRows * kTile * 2];   // [P, dS, what rounding took from dS][key][row of the tile]
-  __shared__ __align__(256) float stat[2][2][kTile];            // [buffer][lse, delta]
+  __shared__ __align__(256) float stat[2][2][kTile];            // [buffer][lse, -delta]
   const int x = blockIdx.x % (a.Hkv * parts), z = blockIdx.x / (a.Hkv * parts);
   const int hk = head_of(x / parts, a.Hkv), pt = x % parts;
   const int g0 = a.Hq / a.Hkv * pt / parts, G = a.Hq / a.Hkv * (pt + 1) / parts - g0;   // heads g0 .. g0+G-1 of the group
@@ -666,7 +666,13 @@ __global__ __launch_bounds__(512, 2) void k_prompt_bwd_kv(PromptArgs a, GradArgs
   auto weigh = [&](int buf, int j, auto masked) __attribute__((always_inline)) {
     const char* qt = lds[buf][0];
     const char* gt = lds[buf][1];
-    f32x16_t s = zero16(), dp = zero16();
+    f32x16_t s = zero16(), dp;                                  // dP starts from -delta
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const f32x4_t dl = *reinterpret_cast<const f32x4_t*>(&stat[buf][1][32 * hf + 8 * b + 4 * h]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dp[4 * b + i] = dl[i];
+    }
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) s = mfma(read_row(qt, of, hf, ks), kf[ks], s);
 #pragma unroll
@@ -674,13 +680,12 @@ __global__ __launch_bounds__(512, 2) void k_prompt_bwd_kv(PromptArgs a, GradArgs
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       const f32x4_t ls = *reinterpret_cast<const f32x4_t*>(&stat[buf][0][32 * hf + 8 * b + 4 * h]);
-      const f32x4_t dl = *reinterpret_cast<const f32x4_t*>(&stat[buf][1][32 * hf + 8 * b + 4 * h]);
       float p[4], ds[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 4 * b + i;
         p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, -ls[i]));
-        ds[i] = p[i] * (dp[r] - dl[i]);
+        ds[i] = p[i] * dp[r];
         if constexpr (decltype(masked)::value) {
           const int q = j * kTile + 32 * hf + reg_row(r) + 4 * h;
           if (q < ki || q >= at.n) p[i] = ds[i] = 0.0f;
