@@ -235,6 +235,11 @@ constexpr int kSoloSteps = 4;
 // Workgroups per compute unit that share the steps, all resident at once: 2
 // (131071 tokens, before non-temporal reads: 34 us; 3 make 39, 4 make 39, 6 make 44).
 constexpr int kWorkers = 2;
+// Steps that starting and ending a unit counts as where the steps are dealt out
+// (a start takes 1.7 us, an end 1.0, a step 1.3).  64 sequences of up to 8192
+// tokens: 62 us with 2 and 3, 69 with 1, 73 with 0; 28 of 1081 tokens on 2 heads,
+// one step a worker: 11.2 with 2, 10.8 with 0.
+constexpr int kUnitCost = 2;
 // Rows up to which the join gives each a workgroup (see k_kv_join's launch).
 constexpr int64_t kWideRows = 1024;
 
@@ -270,7 +275,9 @@ struct Seqs {
     }
     return i;
   }
-  __device__ __forceinline__ int weight(const SeqInfo& i) const { return Hkv * i.tiles * (solo ? 1 : i.steps); }
+  // of one unit: its steps come behind kUnitCost that stand for its start and end
+  __device__ __forceinline__ int share(const SeqInfo& i) const { return solo ? 1 : i.steps > 0 ? i.steps + kUnitCost : 0; }
+  __device__ __forceinline__ int weight(const SeqInfo& i) const { return Hkv * i.tiles * share(i); }
   __device__ __forceinline__ SeqInfo of_lane(int b0) const {    // sequence b0 + lane
     return b0 == 0 ? mine : load(b0 + (threadIdx.x & 63));
   }
@@ -309,6 +316,18 @@ struct Seqs {
       }
       base += __builtin_amdgcn_readlane(incl, 63);
     }
+  }
+};
+
+// `total` steps (or whole units) dealt out to `workers`: the first `extra` take
+// one more than the others.
+struct Deal {
+  int each, extra;
+  __device__ __forceinline__ Deal(int total, int workers) : each(total / workers), extra(total - each * workers) {}
+  __device__ __forceinline__ int begin(int w) const { return w * each + min(w, extra); }
+  __device__ __forceinline__ int owner(int i) const {           // of 0 <= i < total
+    const int more = extra * (each + 1);
+    return i < more ? i / (each + 1) : extra + (i - more) / max(each, 1);
   }
 };
 
@@ -353,9 +372,9 @@ __global__ __launch_bounds__(256, 2) void k_kv_attention(KVCache c, KVSeqs s, co
   const Seqs<MT> seqs(s, c.Hkv, G, cap, solo);
   int total, none;
   seqs.sums(0, total, none);
-  const int per = solo ? 1 : max(1, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
-  int lo = min(static_cast<int64_t>(total), static_cast<int64_t>(blockIdx.x) * per);
-  const int hi = min(total, lo + per);
+  const Deal deal(max(total, 0), gridDim.x);       // negative only where overlapping offsets overflow the counts
+  int lo = deal.begin(blockIdx.x);
+  const int hi = deal.begin(blockIdx.x + 1);
   if (solo && fill && s.offsets) {                 // rows outside every sequence: with a join, it writes them
     const int from = min(max(s.offsets[0], 0), s.T), to = min(max(s.offsets[s.B], from), s.T);
     for (int i = blockIdx.x; i < from + s.T - to; i += gridDim.x) {
@@ -378,9 +397,13 @@ __global__ __launch_bounds__(256, 2) void k_kv_attention(KVCache c, KVSeqs s, co
       ++b;
       continue;
     }
-    const int ns = si.steps, share = solo ? 1 : ns;
+    const int ns = si.steps, share = seqs.share(si);
     if (lo < base) return;                         // only where overlapping offsets overflow the counts
-    const int u = (lo - base) / share, s0 = lo - base - u * share, s1 = solo ? ns : min(ns, s0 + (hi - lo));
+    const int u = (lo - base) / share, from = lo - base - u * share, to = min(share, from + (hi - lo));
+    const int s0 = solo ? 0 : max(0, from - kUnitCost), s1 = solo ? ns : to - kUnitCost;
+    lo += to - from;
+    if (!solo && s0 >= s1) continue;               // none of its steps
+    const bool leading = lo - (to - from) == begin;
     const int rt = u / c.Hkv, h = u - rt * c.Hkv;
     // read by the scalar unit: nothing writes the table while the kernel runs
     typedef const __attribute__((address_space(4))) int32_t table_t;
@@ -651,7 +674,7 @@ __global__ __launch_bounds__(256, 2) void k_kv_attention(KVCache c, KVSeqs s, co
     }
     __syncthreads();
     const bool complete = s0 == 0 && s1 == ns;
-    float* const part = ws + (2 * static_cast<size_t>(blockIdx.x) + (lo == begin ? 0 : 1)) * KVPart<D, MT>::kFloats;
+    float* const part = ws + (2 * static_cast<size_t>(blockIdx.x) + (leading ? 0 : 1)) * KVPart<D, MT>::kFloats;
 #pragma unroll
     for (int k = 0; k < R * D / 1024; ++k) {
       const int idx = k * 256 + threadIdx.x, row = idx / (D / 4), e = 4 * (idx % (D / 4));
@@ -682,7 +705,6 @@ __global__ __launch_bounds__(256, 2) void k_kv_attention(KVCache c, KVSeqs s, co
         }
       }
     }
-    lo += solo ? 1 : s1 - s0;
     __syncthreads();                                               // the results are read before the ring is filled again
   }
 }
@@ -723,16 +745,16 @@ __global__ __launch_bounds__(256) void k_kv_join(KVCache c, KVSeqs s, int Hq, ui
   const Seqs<MT> seqs(s, c.Hkv, G, cap, false);
   int total, before;
   seqs.sums(bb, total, before);
-  const int per = max(1, (total + workers - 1) / workers);
+  const Deal deal(max(total, 0), workers);
   const SeqInfo si = seqs.get(bb);
   if (si.steps == 0) {
     if (tid < LP) *reinterpret_cast<uint2*>(dst + 4 * tid) = make_uint2(0u, 0u);
     return;
   }
   const int h = hq / G, row = (t - si.first) * G + (hq - h * G), rt = row / R, rr = row - rt * R;
-  const int u0 = before + (rt * c.Hkv + h) * si.steps;
-  const int w0 = u0 / per, w1 = (u0 + si.steps - 1) / per;
-  if (u0 < 0 || w1 >= workers) return;                       // only where overlapping offsets overflow the counts
+  const int u0 = before + (rt * c.Hkv + h) * seqs.share(si), at = u0 + kUnitCost;
+  if (u0 < 0 || at > total - si.steps) return;               // only where overlapping offsets overflow the counts
+  const int w0 = deal.owner(at), w1 = deal.owner(at + si.steps - 1);
   if (w0 == w1) return;                                      // one worker wrote the result
   const int grp = tid / LP, e = 4 * (tid % LP);
   Partial p{-INFINITY, 0.0f, {0.f, 0.f, 0.f, 0.f}};
@@ -743,7 +765,7 @@ __global__ __launch_bounds__(256) void k_kv_join(KVCache c, KVSeqs s, int Hq, ui
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int wr = min(w + k * NG, w1);                    // the last one again behind the end, unused
-      const float* part = ws + (2 * static_cast<size_t>(wr) + (wr * per >= u0 ? 0 : 1)) * KVPart<D, MT>::kFloats;
+      const float* part = ws + (2 * static_cast<size_t>(wr) + (deal.begin(wr) >= u0 ? 0 : 1)) * KVPart<D, MT>::kFloats;
       om[k] = part[R * D + rr];
       os[k] = part[R * D + R + rr];
       o[k] = *reinterpret_cast<const f32x4_t*>(part + rr * D + e);
@@ -854,7 +876,7 @@ KVAttnPlan plan_kv_attention(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int3
   const int64_t units = (T * G / (16 * pl.mt) + B) * Hkv, steps = (tokens + kStep - 1) / kStep;
   pl.solo = steps <= kSoloSteps;
   pl.workers = pl.solo ? (units > 0 ? units : 1) : kWorkers * cus;   // one even without sequences: rows outside are filled
-  pl.steps = steps > 0 && units > INT64_MAX / steps ? INT64_MAX : units * (steps > 0 ? steps : 1);
+  pl.steps = steps > 0 && units > INT64_MAX / steps ? INT64_MAX : units * (steps + kUnitCost);
   pl.ws_bytes = pl.solo ? 0 : 2 * static_cast<size_t>(pl.workers) * (16 * pl.mt * (D + 2)) * sizeof(float);
   return pl;
 }
