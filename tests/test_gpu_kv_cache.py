@@ -311,6 +311,18 @@ def test_attention_many_sequences():
         R.within(out[b:b + 1], want, bound, f"sequence {b} of {n}")
 
 
+@pytest.mark.parametrize("count,longest,rows,Hq,Hkv,D", [
+    (7, 700, 1, 4, 2, 128), (100, 1500, 1, 8, 8, 64), (40, 900, 5, 10, 2, 128), (300, 140, 2, 16, 8, 64)])
+def test_attention_work_dealt_out(count, longest, rows, Hq, Hkv, D):
+    """Fewer steps than workers, a few each and many each; sequences that one
+    worker takes whole, ends in or begins in, and empty ones between them."""
+    g = np.random.default_rng(count)
+    lens = [int(x) for x in g.integers(1, longest + 1, count)]
+    lens[2], lens[3], lens[count // 2] = 0, 1, longest
+    new = [min(n, rows) for n in lens]
+    check_attention(lens, new, Hq, Hkv, D, 16)
+
+
 def test_attention_large_scores_and_scale():
     check_attention([300, 70], None, 4, 2, 128, 16, qscale=30.0)
     check_attention([300, 70], None, 4, 2, 128, 16, scale=0.01)
