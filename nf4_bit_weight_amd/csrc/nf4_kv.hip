@@ -222,10 +222,8 @@ __global__ __launch_bounds__(256) void k_kv_dequantize(KVCache c, KVSeqs s, uint
 //
 // Bound by memory: 4.5 bits an element (72 bytes a vector of 128), read once a
 // unit.  131071 tokens, 32 heads on 8: 32 us for 151 MB (4.8 TB/s) and 4.4 us
-// for the join; 64 sequences of up to 8192 tokens: 71 us for 302 MB.  About 240
-// vector instructions per 32 tokens and wave, half of what the same stream
-// would need with a 16-entry table looked up by byte permutes in place of the
-// hardware conversion.
+// for the join; 64 sequences of up to 8192 tokens: 60 us for 302 MB.  About 250
+// vector instructions per 32 tokens and wave.
 constexpr int kStep = 128;           // tokens per workgroup step, 32 a wave
 constexpr float kSlack = 8.0f;       // see the running maximum below
 // Units of at most this many steps are taken whole, without a join.  One

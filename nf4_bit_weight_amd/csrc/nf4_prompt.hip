@@ -281,7 +281,7 @@ __device__ __forceinline__ int head_of(int x, int heads) { return heads % 8 == 0
 // One workgroup: 128 query rows of one head, streaming keys and values.  Bound
 // by the matrix and vector units together (a 64-key tile is 1024 cycles of
 // products and about 900 of exponentials and sums a wave, two waves a SIMD):
-// 8192 rows, 32 heads on 8 of 128: 516 us, 1065 TFLOP/s, where this card's
+// 8192 rows, 32 heads on 8 of 128: 488 to 516 us, 1065 to 1127 TFLOP/s, where this card's
 // library product of 8192 cubed reaches 1240.  The running maximum moves only when a score passes it by 2^kSlack, so the
 // rescaling of the sums is rare; weights are then at most 2^kSlack, which
 // costs bf16 and fp32 nothing.
@@ -468,8 +468,8 @@ struct GradArgs {
 
 // grad_q: a wave keeps 32 query rows and streams keys and values.
 //   delta = dO . O, P = exp(scale S - lse), dS = P (dO V^T - delta), grad_q = scale dS K
-// 9195 rows in 6 sequences, 32 heads on 8 of 128: 231 us (3 products, 845
-// TFLOP/s), 7 of them for what rounding took on the diagonal; with S and dP
+// 9195 rows in 6 sequences, 32 heads on 8 of 128: 221 to 231 us (3 products, 845
+// TFLOP/s and more), 7 of them for what rounding took on the diagonal; with S and dP
 // formed together, one product each in turn, 16 more.
 template <int D>
 __global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, GradArgs g, uint16_t* __restrict__ gq, int bound) {
@@ -602,8 +602,8 @@ __global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, GradArgs 
 // rows and leaves them in LDS (bf16); then each multiplies the whole tile into
 // its half of the elements of grad_v and grad_k.  So the sums of a wave take 64
 // registers, not 128, and two waves fit a SIMD, one's exponentials under the
-// other's products.  9195 rows in 6 sequences, 32 heads on 8 of 128: 325 us
-// (4 products, 800 TFLOP/s), 17 of them for what rounding took on the diagonal;
+// other's products.  9195 rows in 6 sequences, 32 heads on 8 of 128: 317 to 325
+// us (4 products, 800 TFLOP/s and more), 17 of them for what rounding took on the diagonal;
 // 4 waves that keep all sums, one a SIMD, took 360 without that.
 // Where the tiles alone leave compute units idle, the heads of a group are
 // split over `parts` workgroups, whose fp32 sums k_prompt_join adds in order.
