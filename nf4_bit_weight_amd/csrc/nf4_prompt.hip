@@ -551,6 +551,10 @@ __global__ __launch_bounds__(256, 2) void k_prompt_bwd_q(PromptArgs a, GradArgs 
       if constexpr (decltype(masked)::value)
         if (j * kTile + 32 * w + reg_row(r) + 4 * h > qi) p.s[r] = 0.0f;
     }
+    // the first row sees one key: its weight is 1 whatever the score, the score's
+    // gradient zero, not what two orders of the same sum differ by (a NaN stays)
+    if constexpr (decltype(masked)::value)
+      if (qi == 0) p.s[0] *= 0.0f;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const bf16x8_t pf = pack8(p.s, m);
@@ -691,6 +695,7 @@ __global__ __launch_bounds__(512, 2) void k_prompt_bwd_kv(PromptArgs a, GradArgs
         if constexpr (decltype(masked)::value) {
           const int q = j * kTile + 32 * hf + reg_row(r) + 4 * h;
           if (q < ki || q >= at.n) p[i] = ds[i] = 0.0f;
+          if (r == 0 && q == 0) ds[i] *= 0.0f;                  // as in grad_q's kernel
         }
       }
       const int at_q = wrow + (((4 * hf + b) ^ (l32 & 7)) << 4) + 8 * h;

@@ -378,3 +378,34 @@ def test_capture_refuses_leaves_of_a_living_eager_graph():
     assert torch.equal(out, alive.detach())
     grads = torch.autograd.grad(alive, xs, torch.ones_like(alive))
     assert all(g.isfinite().all() for g in grads)
+
+
+@pytest.mark.parametrize("lens", [[1], [1] * 8, [1, 40, 1, 129]])
+@pytest.mark.parametrize("Hq,Hkv,D", [(12, 4, 64), (4, 4, 128)])
+def test_a_single_key_has_no_score_gradient(lens, Hq, Hkv, D):
+    """A row that sees one key weighs it with 1: exactly no gradient reaches its
+    query, and its key gets none from it."""
+    _, q, k, v = inputs(lens, Hq, Hkv, D, seed=11)
+    off = R.offsets_of(lens).to(DEV)
+    xs = [x.to(DEV).contiguous().requires_grad_() for x in (q, k, v)]
+    gy = R.normal(95, sum(lens), Hq, D).to(DEV)
+    gq, gk, gv = torch.autograd.grad(nf4_prompt_attention(*xs, off), xs, gy)
+    first = off[:-1].long()
+    assert not gq[first].any()
+    alone = first[torch.tensor([n == 1 for n in lens], device=DEV)]
+    assert not gk[alone].any()
+    # grad_v there is the sum of the group's output gradients, rounded once
+    want = gy[alone].double().unflatten(1, (Hkv, Hq // Hkv))
+    room = (R.U + 2.0 ** -20) * want.abs().sum(2)
+    assert ((gv[alone].double() - want.sum(2)).abs() <= room).all()
+
+
+def test_a_nan_score_of_a_single_key_is_not_hidden():
+    _, q, k, v = inputs([1, 5], 2, 2, 64, seed=12)
+    q[0, 0, 3] = float("nan")
+    xs = [x.to(DEV).contiguous().requires_grad_() for x in (q, k, v)]
+    off = R.offsets_of([1, 5]).to(DEV)
+    out = nf4_prompt_attention(*xs, off)
+    gq, _, _ = torch.autograd.grad(out, xs, torch.ones_like(out))
+    assert out[0, 0].isnan().all() and gq[0, 0].isnan().all()
+    assert out[1:].isfinite().all() and gq[1:].isfinite().all()
