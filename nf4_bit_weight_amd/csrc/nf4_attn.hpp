@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "nf4_deal.hpp"
 #include "nf4_device.hpp"
 
 namespace nf4 {
@@ -112,12 +113,12 @@ __device__ __forceinline__ int lane_move(int x) {
   return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, false);
 }
 __device__ __forceinline__ int wave_scan(int x) {
-  x += lane_move<0x111, 0xF>(x);   // row_shr:1
-  x += lane_move<0x112, 0xF>(x);
-  x += lane_move<0x114, 0xF>(x);
-  x += lane_move<0x118, 0xF>(x);
-  x += lane_move<0x142, 0xA>(x);   // row_bcast:15 into rows 1 and 3
-  x += lane_move<0x143, 0xC>(x);   // row_bcast:31 into rows 2 and 3
+  x = wrap_add(x, lane_move<0x111, 0xF>(x));   // row_shr:1
+  x = wrap_add(x, lane_move<0x112, 0xF>(x));
+  x = wrap_add(x, lane_move<0x114, 0xF>(x));
+  x = wrap_add(x, lane_move<0x118, 0xF>(x));
+  x = wrap_add(x, lane_move<0x142, 0xA>(x));   // row_bcast:15 into rows 1 and 3
+  x = wrap_add(x, lane_move<0x143, 0xC>(x));   // row_bcast:31 into rows 2 and 3
   return x;
 }
 __device__ __forceinline__ int wave_sum(int x) { return __builtin_amdgcn_readlane(wave_scan(x), 63); }
@@ -164,27 +165,14 @@ __device__ __forceinline__ float quad_sum(float x) {
   return a[0] + a[1];
 }
 
-// The rows of sequence b, clamped into 0 .. T whatever the offsets hold.
-__device__ __forceinline__ void seq_rows(const int32_t* offsets, int b, int T, int& first, int& n) {
-  if (!offsets) {
-    first = b;
-    n = b < T ? 1 : 0;
-    return;
-  }
-  const int s = min(max(offsets[b], 0), T), e = min(max(offsets[b + 1], s), T);
-  first = s;
-  n = e - s;
-}
-
 // The sequence that row t belongs to, or -1 (all lanes of the wave take part
-// and t is the same in all of them): the last b with offsets[b] <= t.
+// and t is the same in all of them).
 __device__ __forceinline__ int seq_of(const int32_t* offsets, int B, int T, int t) {
   if (!offsets) return t < B ? t : -1;
   int count = 0;
   for (int i = threadIdx.x & 63; i - (int)(threadIdx.x & 63) <= B; i += 64)
     count += __popcll(__ballot(i <= B && offsets[min(i, B)] <= t));
-  const int b = count - 1;
-  return (b >= 0 && b < B && t < offsets[b + 1]) ? b : -1;
+  return owner_of(offsets, B, t, count);
 }
 
 }  // namespace nf4

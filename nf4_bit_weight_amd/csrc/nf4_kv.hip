@@ -275,7 +275,7 @@ struct Seqs {
   }
   // of one unit: its steps come behind kUnitCost that stand for its start and end
   __device__ __forceinline__ int share(const SeqInfo& i) const { return solo ? 1 : i.steps > 0 ? i.steps + kUnitCost : 0; }
-  __device__ __forceinline__ int weight(const SeqInfo& i) const { return Hkv * i.tiles * share(i); }
+  __device__ __forceinline__ int weight(const SeqInfo& i) const { return wrap_mul(Hkv * i.tiles, share(i)); }
   __device__ __forceinline__ SeqInfo of_lane(int b0) const {    // sequence b0 + lane
     return b0 == 0 ? mine : load(b0 + (threadIdx.x & 63));
   }
@@ -293,8 +293,8 @@ struct Seqs {
     int sum = 0, pre = 0;
     for (int b0 = 0; b0 < s.B; b0 += 64) {
       const int w = weight(of_lane(b0));
-      sum += w;
-      if (b0 + static_cast<int>(threadIdx.x & 63) < upto) pre += w;
+      sum = wrap_add(sum, w);
+      if (b0 + static_cast<int>(threadIdx.x & 63) < upto) pre = wrap_add(pre, w);
     }
     total = wave_sum(sum);
     before = wave_sum(pre);
@@ -305,27 +305,15 @@ struct Seqs {
     base = 0;
     for (int b0 = 0; b0 < s.B; b0 += 64) {
       const int w = weight(of_lane(b0)), incl = wave_scan(w);
-      const uint64_t hit = __ballot(base + incl > lo);
+      const uint64_t hit = __ballot(wrap_add(base, incl) > lo);
       if (hit) {
         const int l = __builtin_ctzll(hit);
         b = b0 + l;
-        base += __builtin_amdgcn_readlane(incl - w, l);
+        base = wrap_add(base, __builtin_amdgcn_readlane(wrap_sub(incl, w), l));
         return;
       }
-      base += __builtin_amdgcn_readlane(incl, 63);
+      base = wrap_add(base, __builtin_amdgcn_readlane(incl, 63));
     }
-  }
-};
-
-// `total` steps (or whole units) dealt out to `workers`: the first `extra` take
-// one more than the others.
-struct Deal {
-  int each, extra;
-  __device__ __forceinline__ Deal(int total, int workers) : each(total / workers), extra(total - each * workers) {}
-  __device__ __forceinline__ int begin(int w) const { return w * each + min(w, extra); }
-  __device__ __forceinline__ int owner(int i) const {           // of 0 <= i < total
-    const int more = extra * (each + 1);
-    return i < more ? i / (each + 1) : extra + (i - more) / max(each, 1);
   }
 };
 
@@ -390,14 +378,16 @@ __global__ __launch_bounds__(256, 2) void k_kv_attention(KVCache c, KVSeqs s, co
   while (lo < hi && b < s.B) {
     const SeqInfo si = seqs.get(b);
     const int n = si.n, len = si.len, first = si.first, weight = seqs.weight(si);
-    if (lo >= base + weight) {                     // nothing (left) of this sequence
-      base += weight;
+    const int end = wrap_add(base, weight);
+    if (lo >= end) {                               // nothing (left) of this sequence
+      base = end;
       ++b;
       continue;
     }
     const int ns = si.steps, share = seqs.share(si);
-    if (lo < base) return;                         // only where overlapping offsets overflow the counts
-    const int u = (lo - base) / share, from = lo - base - u * share, to = min(share, from + (hi - lo));
+    UnitAt at_unit;
+    if (!unit_at(lo, hi, base, c.Hkv * si.tiles, share, at_unit)) return;   // only where overlapping offsets overflow the counts
+    const int u = at_unit.u, from = at_unit.from, to = at_unit.to;
     const int s0 = solo ? 0 : max(0, from - kUnitCost), s1 = solo ? ns : to - kUnitCost;
     lo += to - from;
     if (!solo && s0 >= s1) continue;               // none of its steps
@@ -750,9 +740,9 @@ __global__ __launch_bounds__(256) void k_kv_join(KVCache c, KVSeqs s, int Hq, ui
     return;
   }
   const int h = hq / G, row = (t - si.first) * G + (hq - h * G), rt = row / R, rr = row - rt * R;
-  const int u0 = before + (rt * c.Hkv + h) * seqs.share(si), at = u0 + kUnitCost;
-  if (u0 < 0 || at > total - si.steps) return;               // only where overlapping offsets overflow the counts
-  const int w0 = deal.owner(at), w1 = deal.owner(at + si.steps - 1);
+  SharedBy by;
+  if (!shared_by(rt * c.Hkv + h, seqs.share(si), kUnitCost, before, total, deal, by)) return;   // as in k_kv_attention
+  const int u0 = by.u0, w0 = by.w0, w1 = by.w1;
   if (w0 == w1) return;                                      // one worker wrote the result
   const int grp = tid / LP, e = 4 * (tid % LP);
   Partial p{-INFINITY, 0.0f, {0.f, 0.f, 0.f, 0.f}};
