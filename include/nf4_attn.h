@@ -44,6 +44,10 @@
  * block with top < 2^-120 is kept as zeros (scale 0); one that holds a NaN or
  * an infinity is kept as NaN (scale NaN, patterns 0).
  *
+ * Range.  The forward calls keep every softmax weight at or below 1 / 2n, n the
+ * tokens that a row may see, so that sums over finite values of any size are
+ * finite; what falls below 2^-126 in them is at most n^2 2^-113 in a result.
+ *
  * A workspace belongs to one call at a time: calls that may overlap (other
  * streams, graphs replayed side by side) take different ones.
  *

@@ -76,6 +76,18 @@ hipError_t launch_prompt_bwd(const PromptArgs& a, const void* grad_out, int64_t 
 
 // ---- device helpers ----------------------------------------------------------
 
+// The softmax of the forward kernels, in units of log2.  The maximum in use
+// moves only when a score passes it by kSlack, so that the sums are rarely
+// rescaled; weights are then up to 2^kSlack times those of the true maximum.
+// It is carried with headroom(n) on top, n the number of tokens that a row may
+// see: no weight passes 1 / 2n, and sums over values of any finite size stay
+// finite.  A power of two, so no bit of a weight is lost; products of a weight and
+// a value that fall below 2^-126 are, together at most n^2 2^-113 in a result.
+constexpr float kSlack = 8.0f;
+__device__ __forceinline__ float headroom(int n) {
+  return kSlack + static_cast<float>(33 - __builtin_clz(static_cast<unsigned>(larger(n, 1))));
+}
+
 // Copies straight into LDS, invisible to the compiler's own waits; the kernels
 // wait for them themselves.  The LDS address is uniform, lane i lands 16 i
 // (4 i) bytes behind it.

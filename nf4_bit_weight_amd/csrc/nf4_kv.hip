@@ -225,7 +225,6 @@ __global__ __launch_bounds__(256) void k_kv_dequantize(KVCache c, KVSeqs s, uint
 // for the join; 64 sequences of up to 8192 tokens: 60 us for 302 MB.  About 250
 // vector instructions per 32 tokens and wave.
 constexpr int kStep = 128;           // tokens per workgroup step, 32 a wave
-constexpr float kSlack = 8.0f;       // see the running maximum below
 // Units of at most this many steps are taken whole, without a join.  One
 // sequence, 32 heads on 8, whole and shared: 256 tokens 5.8 and 8.1 us, 512
 // tokens 7.8 and 8.2, 1024 tokens 11.9 and 8.3.
@@ -397,6 +396,7 @@ __global__ __launch_bounds__(256, 2) void k_kv_attention(KVCache c, KVSeqs s, co
     typedef const __attribute__((address_space(4))) int32_t table_t;
     table_t* pt = (table_t*)(s.table + static_cast<int64_t>(b) * s.width);
     const int seen = min(max(len, 0), cap);
+    const float room = headroom(seen);             // the same for all workers of the sequence
 
     // queries: row rt * R + 16 mt + (lane & 15), elements 16 g .. of each block, pairs swapped as the conversion
     // gives them
@@ -538,7 +538,7 @@ __global__ __launch_bounds__(256, 2) void k_kv_attention(KVCache c, KVSeqs s, co
               p[m][w][i] = ((ok >> w) & 1) && t0 + 16 * w + 4 * g + i <= lim[m] ? p[m][w][i] : -INFINITY;
         }
         float top = fmaxf(fmaxf(fmaxf(p[m][0][0], p[m][0][1]), p[m][0][2]), fmaxf(fmaxf(p[m][0][3], p[m][1][0]), p[m][1][1]));
-        top = quad_max(fmaxf(fmaxf(top, p[m][1][2]), p[m][1][3])) * scale2;
+        top = __builtin_fmaf(quad_max(fmaxf(fmaxf(top, p[m][1][2]), p[m][1][3])), scale2, room);
         // the maximum in use moves only when a score passes it by 2^kSlack
         if (__any(top > mx[m] + kSlack)) {
           const float to = fmaxf(top, mx[m]), f = to == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[m] - to);

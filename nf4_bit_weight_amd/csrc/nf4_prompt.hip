@@ -282,11 +282,7 @@ __device__ __forceinline__ int head_of(int x, int heads) { return heads % 8 == 0
 // by the matrix and vector units together (a 64-key tile is 1024 cycles of
 // products and about 900 of exponentials and sums a wave, two waves a SIMD):
 // 8192 rows, 32 heads on 8 of 128: 488 to 516 us, 1065 to 1127 TFLOP/s, where this card's
-// library product of 8192 cubed reaches 1240.  The running maximum moves only when a score passes it by 2^kSlack, so the
-// rescaling of the sums is rare; weights are then at most 2^kSlack, which
-// costs bf16 and fp32 nothing.
-constexpr float kSlack = 8.0f;
-
+// library product of 8192 cubed reaches 1240.
 template <int D>
 __global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* __restrict__ out,
                                                        uint16_t* __restrict__ rest, float* __restrict__ lse, int bound) {
@@ -316,7 +312,8 @@ __global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* _
   f32x16_t acc[DT];
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt) acc[dt] = zero16();
-  float ref = -INFINITY, sum[2] = {0.0f, 0.0f};                 // ref: the maximum in use, times c
+  const float room = headroom(at.n);
+  float ref = -INFINITY, sum[2] = {0.0f, 0.0f};                 // ref: the maximum in use, times c, and room
 
   auto scores = [&](int j, f32x16_t (&s)[2]) __attribute__((always_inline)) {
     const char* kt = lds[j & 1][0];
@@ -331,7 +328,7 @@ __global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* _
     float top = s[0][0];
 #pragma unroll
     for (int r = 1; r < 31; r += 2) top = fmaxf(fmaxf(top, s[r / 16][r % 16]), s[(r + 1) / 16][(r + 1) % 16]);
-    top = half_max(fmaxf(top, s[1][15])) * c;
+    top = __builtin_fmaf(half_max(fmaxf(top, s[1][15])), c, room);
     if (__any(top > ref + kSlack)) {
       const float to = fmaxf(top, ref), f = to == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ref - to);
       sum[0] *= f;
