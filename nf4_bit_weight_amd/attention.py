@@ -17,6 +17,8 @@ Tensor conventions (all on one CUDA/HIP device):
   page_table      int32 [B, width], the pages that hold a sequence's tokens
 Rows outside every sequence are zeros in a result allocated here and left as
 they were in one that is passed in.
+
+No call has a forward derivative: inputs with a forward-mode tangent are refused.
 """
 
 from __future__ import annotations

@@ -107,6 +107,7 @@ def nf4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offs
     q, k and v, once.  The kernels compute in bf16 with fp32 accumulation; the
     output and the gradients come back in the dtypes that the caller passed in.
     Rows outside every sequence are zeros in both.
+    Forward-mode tangents are refused.
 
     Forward and backward can be captured into a graph together.  No eager graph
     of the same leaves may live then: its gradient accumulators belong to the

@@ -58,6 +58,14 @@ long long integer(PyObject* o, const char* name) {
 }
 bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
 
+// No call has a forward derivative: a tangent would be lost without a word.
+using Named = std::initializer_list<std::pair<const char*, PyObject*>>;
+void no_tangents(const Named& inputs) {
+  for (const auto& [name, o] : inputs)
+    if (given(o) && tensor(o, name)._fw_grad(0).defined())
+      refuse(name, " carries a forward-mode tangent, and this call has no forward derivative");
+}
+
 void need(const Tensor& t, const char* name, at::ScalarType dtype, int64_t numel, const c10::Device* device) {
   if (!t.is_cuda()) refuse(name, " must be a device tensor");
   if (!t.is_contiguous()) refuse(name, " must be contiguous");
@@ -217,6 +225,7 @@ PyObject* several(const T&... t) {
 
 // (k_codes, k_scale, v_codes, v_scale, k, v, lengths, page_table, offsets, inv_freq, interleaved, q, return_k, q_out, k_out)
 PyObject* kv_append(PyObject* const* a) {
+  no_tangents({{"k_scale", a[1]}, {"v_scale", a[3]}, {"k", a[4]}, {"v", a[5]}, {"inv_freq", a[9]}, {"q", a[11]}});
   const Cache c = cache_of(a);
   const Rows k = rows_of(a[4], "k", c.H, c.D, -1, c.dev), v = rows_of(a[5], "v", c.H, c.D, k.T, c.dev);
   const Seqs s = seqs_of(a[6], a[7], a[8], k.T, c.dev);
@@ -256,6 +265,7 @@ PyObject* kv_append(PyObject* const* a) {
 
 // (k_codes, k_scale, v_codes, v_scale, lengths, page_table, offsets, rows, k_out, v_out)
 PyObject* kv_dequantize(PyObject* const* a) {
+  no_tangents({{"k_scale", a[1]}, {"v_scale", a[3]}});
   const Cache c = cache_of(a);
   int64_t T;
   if (given(a[7])) {
@@ -276,6 +286,7 @@ PyObject* kv_dequantize(PyObject* const* a) {
 
 // (k_codes, k_scale, v_codes, v_scale, q, lengths, page_table, offsets, scale, out, ws)
 PyObject* kv_attention(PyObject* const* a) {
+  no_tangents({{"k_scale", a[1]}, {"v_scale", a[3]}, {"q", a[4]}});
   const Cache c = cache_of(a);
   const Rows q = rows_of(a[4], "q", -1, c.D, -1, c.dev);
   const int32_t Hq = groups(q.H, c.H);
@@ -344,6 +355,7 @@ int run_backward(const Prompt& p, const Tensor& grad_out, const Tensor& out, con
 
 // (q, k, v, offsets, scale, out, for_backward)
 PyObject* prompt_fwd(PyObject* const* a) {
+  no_tangents({{"q", a[0]}, {"k", a[1]}, {"v", a[2]}});
   const Prompt p = prompt_of(tensor(a[0], "q"), tensor(a[1], "k"), tensor(a[2], "v"), tensor(a[3], "offsets"), scale_arg(a[4]));
   bool fill;
   const Tensor out = result(a[5], "out", p.q.T, p.q.H, p.D, p.dev, fill);
@@ -360,6 +372,7 @@ PyObject* prompt_fwd(PyObject* const* a) {
 
 // (grad_out, q, k, v, out, out_rest, lse, offsets, scale, ws)
 PyObject* prompt_bwd(PyObject* const* a) {
+  no_tangents({{"grad_out", a[0]}, {"q", a[1]}, {"k", a[2]}, {"v", a[3]}, {"out", a[4]}, {"out_rest", a[5]}, {"lse", a[6]}});
   const Prompt p = prompt_of(tensor(a[1], "q"), tensor(a[2], "k"), tensor(a[3], "v"), tensor(a[7], "offsets"), scale_arg(a[8]));
   Grads g;
   const int st = run_backward(p, tensor(a[0], "grad_out"), tensor(a[4], "out"), given(a[5]) ? tensor(a[5], "out_rest") : Tensor(),
@@ -403,6 +416,8 @@ struct PromptAttention : torch::autograd::Function<PromptAttention> {
   static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx, torch::autograd::variable_list grad) {
     if (at::GradMode::is_enabled())
       throw std::runtime_error("nf4_prompt_attention: its backward pass is not differentiable (create_graph)");
+    if (grad[0].defined() && grad[0]._fw_grad(0).defined())
+      throw std::runtime_error("nf4_prompt_attention: grad_out carries a forward-mode tangent, and the backward pass has no forward derivative");
     const auto s = ctx->get_saved_variables();
     const Prompt p = prompt_of(s[0], s[1], s[2], s[6], ctx->saved_data["scale"].toDouble());
     Grads g;
@@ -433,6 +448,7 @@ void check_capture(std::initializer_list<std::pair<const char*, const Tensor*>> 
 
 // (q, k, v, offsets, scale): any floating dtype and layout, differentiable
 PyObject* prompt_attention(PyObject* const* a) {
+  no_tangents({{"q", a[0]}, {"k", a[1]}, {"v", a[2]}});
   const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &offsets = tensor(a[3], "offsets");
   for (const Tensor* t : {&q, &k, &v})
     if (!t->is_cuda()) refuse("q, k and v must be device tensors");
