@@ -19,6 +19,11 @@ Rows outside every sequence are zeros in a result allocated here and left as
 they were in one that is passed in.
 
 No call has a forward derivative: inputs with a forward-mode tangent are refused.
+The cache calls have no gradient: while gradients are recorded, inputs that
+require one are refused (detach them, or call under torch.no_grad()); a training
+step rotates in torch.  nf4_prompt_attention_fwd and _bwd are the two halves that
+autograd.nf4_prompt_attention records; called by themselves they record nothing,
+like nf4_matmul_fwd.
 """
 
 from __future__ import annotations

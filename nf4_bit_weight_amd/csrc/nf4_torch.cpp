@@ -66,6 +66,16 @@ void no_tangents(const Named& inputs) {
       refuse(name, " carries a forward-mode tangent, and this call has no forward derivative");
 }
 
+// Rotation and cache have no gradient either: an input that wants one is refused
+// while gradients are recorded, not returned without its history.
+void no_derivatives(const Named& inputs) {
+  no_tangents(inputs);
+  if (!at::GradMode::is_enabled()) return;
+  for (const auto& [name, o] : inputs)
+    if (given(o) && tensor(o, name).requires_grad())
+      refuse(name, " requires a gradient, which this call does not carry: detach it, or call under torch.no_grad()");
+}
+
 void need(const Tensor& t, const char* name, at::ScalarType dtype, int64_t numel, const c10::Device* device) {
   if (!t.is_cuda()) refuse(name, " must be a device tensor");
   if (!t.is_contiguous()) refuse(name, " must be contiguous");
@@ -225,7 +235,7 @@ PyObject* several(const T&... t) {
 
 // (k_codes, k_scale, v_codes, v_scale, k, v, lengths, page_table, offsets, inv_freq, interleaved, q, return_k, q_out, k_out)
 PyObject* kv_append(PyObject* const* a) {
-  no_tangents({{"k_scale", a[1]}, {"v_scale", a[3]}, {"k", a[4]}, {"v", a[5]}, {"inv_freq", a[9]}, {"q", a[11]}});
+  no_derivatives({{"k_scale", a[1]}, {"v_scale", a[3]}, {"k", a[4]}, {"v", a[5]}, {"inv_freq", a[9]}, {"q", a[11]}});
   const Cache c = cache_of(a);
   const Rows k = rows_of(a[4], "k", c.H, c.D, -1, c.dev), v = rows_of(a[5], "v", c.H, c.D, k.T, c.dev);
   const Seqs s = seqs_of(a[6], a[7], a[8], k.T, c.dev);
@@ -265,7 +275,7 @@ PyObject* kv_append(PyObject* const* a) {
 
 // (k_codes, k_scale, v_codes, v_scale, lengths, page_table, offsets, rows, k_out, v_out)
 PyObject* kv_dequantize(PyObject* const* a) {
-  no_tangents({{"k_scale", a[1]}, {"v_scale", a[3]}});
+  no_derivatives({{"k_scale", a[1]}, {"v_scale", a[3]}});
   const Cache c = cache_of(a);
   int64_t T;
   if (given(a[7])) {
@@ -286,7 +296,7 @@ PyObject* kv_dequantize(PyObject* const* a) {
 
 // (k_codes, k_scale, v_codes, v_scale, q, lengths, page_table, offsets, scale, out, ws)
 PyObject* kv_attention(PyObject* const* a) {
-  no_tangents({{"k_scale", a[1]}, {"v_scale", a[3]}, {"q", a[4]}});
+  no_derivatives({{"k_scale", a[1]}, {"v_scale", a[3]}, {"q", a[4]}});
   const Cache c = cache_of(a);
   const Rows q = rows_of(a[4], "q", -1, c.D, -1, c.dev);
   const int32_t Hq = groups(q.H, c.H);

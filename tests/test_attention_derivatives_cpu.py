@@ -54,3 +54,21 @@ def test_forward_mode_tangents_are_refused():
                 call()
         with pytest.raises(ValueError, match="device"):
             nf4_prompt_attention(X, X, X, I)
+
+
+def test_cache_calls_refuse_to_cut_a_graph():
+    """Rotation and cache have no gradient: while gradients are recorded, inputs
+    that want one are refused, not returned without their history."""
+    def leaf(t):
+        return t.clone().requires_grad_()
+    for call in cache_calls(leaf):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="device"):           # nothing is recorded: an ordinary call
+            call()
+    for call in cache_calls(lambda t: (leaf(t) * 1.0)):                             # a result further down
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    for call in cache_calls(lambda t: leaf(t).detach()):
+        with pytest.raises(ValueError, match="device"):
+            call()
