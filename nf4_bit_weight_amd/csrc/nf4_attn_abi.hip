@@ -39,14 +39,38 @@ int check_rows(const void* p, int64_t stride, int64_t T) {
   return NF4_OK;
 }
 
+// Positions in a page table are counted in 32 bits.
+int check_table(int32_t width, int32_t page) {
+  if (width < 0 || page < 1) return NF4_ERR_SHAPE;
+  if (page % 16 || static_cast<int64_t>(width) * page > INT32_MAX - 256) return NF4_ERR_UNSUPPORTED;
+  return NF4_OK;
+}
+
+// Sizes of a cache attention call, and how it is cut.
+int check_plan(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t width, int32_t page, KVAttnPlan& pl) {
+  int st = check_heads(T, B, Hq, Hkv, D);
+  if (!st) st = check_table(width, page);
+  if (st || T == 0) return st;
+  pl = plan_kv_attention(T, B, Hq, Hkv, D, static_cast<int64_t>(width) * page, device_cu_count());
+  // units and their steps of 128 tokens are counted in 32 bits
+  if (pl.steps > INT32_MAX / 2 || !launchable(pl.workers, 256)) return NF4_ERR_UNSUPPORTED;
+  if (!pl.solo && !launchable(kv_join_groups(T, Hq), 256)) return NF4_ERR_UNSUPPORTED;
+  return NF4_OK;
+}
+
+// Sizes of the prompt's calls: grad_k's workgroups are of 512 threads and split
+// the heads of a group at most to one each.
+int check_prompt(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int64_t threads) {
+  const int st = check_heads(T, B, Hq, Hkv, D);
+  return st || T == 0 ? st : launchable(prompt_groups(T, B, Hq), threads) ? NF4_OK : NF4_ERR_UNSUPPORTED;
+}
+
 int check_seqs(int64_t T, const int32_t* offsets, const int32_t* lengths, int32_t B, const int32_t* table,
                int32_t width, int32_t page) {
-  if (width < 0) return NF4_ERR_SHAPE;
   if (!offsets && T != B) return NF4_ERR_SHAPE;
   if (B > 0 && (!lengths || (width > 0 && !table))) return NF4_ERR_NULL;
   if (!aligned(offsets, 4) || !aligned(lengths, 4) || !aligned(table, 4)) return NF4_ERR_ALIGN;
-  if (static_cast<int64_t>(width) * page > INT32_MAX - 256) return NF4_ERR_UNSUPPORTED;
-  return NF4_OK;
+  return check_table(width, page);
 }
 
 int check_cache(const void* kc, const void* ks, const void* vc, const void* vs, int64_t P, int32_t page) {
@@ -116,9 +140,8 @@ int nf4_kv_dequantize(int64_t T, const int32_t* offsets, const int32_t* lengths,
 
 size_t nf4_kv_attention_workspace(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t width,
                                   int32_t page) {
-  if (check_heads(T, B, Hq, Hkv, D) || width < 0 || page < 1) return SIZE_MAX;
-  if (T == 0) return 0;
-  return plan_kv_attention(T, B, Hq, Hkv, D, static_cast<int64_t>(width) * page, device_cu_count()).ws_bytes;
+  KVAttnPlan pl{};
+  return check_plan(T, B, Hq, Hkv, D, width, page, pl) ? SIZE_MAX : pl.ws_bytes;
 }
 
 int nf4_kv_attention(const void* q, int64_t q_stride, int64_t T, int32_t Hq, const int32_t* offsets,
@@ -136,10 +159,9 @@ int nf4_kv_attention(const void* q, int64_t q_stride, int64_t T, int32_t Hq, con
   if (!aligned(out, 16)) return NF4_ERR_ALIGN;
   if (T == 0) return NF4_OK;
   if (P == 0) width = 0;                                     // no pages: no key is seen (and no workspace is needed)
-  const KVAttnPlan pl = plan_kv_attention(T, B, Hq, Hkv, D, static_cast<int64_t>(width) * page, device_cu_count());
-  // units and their steps of 128 tokens are counted in 32 bits
-  if (pl.steps > INT32_MAX / 2 || !launchable(pl.workers, 256)) return NF4_ERR_UNSUPPORTED;
-  if (!pl.solo && !launchable(kv_join_groups(T, Hq), 256)) return NF4_ERR_UNSUPPORTED;
+  KVAttnPlan pl{};
+  st = check_plan(T, B, Hq, Hkv, D, width, page, pl);
+  if (st) return st;
   if (pl.ws_bytes > 0 && (!ws || ws_bytes < pl.ws_bytes)) return NF4_ERR_WORKSPACE;
   if (pl.ws_bytes > 0 && !aligned(ws, 16)) return NF4_ERR_ALIGN;
   const KVCache c{const_cast<uint8_t*>(k_codes), const_cast<float*>(k_scale), const_cast<uint8_t*>(v_codes),
@@ -155,7 +177,7 @@ int nf4_prompt_attention_fwd(const void* q, int64_t q_stride, const void* k, int
                              int64_t v_stride, int64_t T, const int32_t* offsets, int32_t B, int32_t Hq, int32_t Hkv,
                              int32_t D, float scale, void* out, void* out_rest, float* lse, int fill_outside,
                              void* stream) {
-  int st = check_heads(T, B, Hq, Hkv, D);
+  int st = check_prompt(T, B, Hq, Hkv, D, 256);
   if (!st) st = check_rows(q, q_stride, T);
   if (!st) st = check_rows(k, k_stride, T);
   if (!st) st = check_rows(v, v_stride, T);
@@ -164,7 +186,6 @@ int nf4_prompt_attention_fwd(const void* q, int64_t q_stride, const void* k, int
   if (!offsets || (T > 0 && !out)) return NF4_ERR_NULL;
   if (!aligned(out, 16) || !aligned(out_rest, 16) || !aligned(lse, 4) || !aligned(offsets, 4)) return NF4_ERR_ALIGN;
   if (T == 0) return NF4_OK;
-  if (!launchable(prompt_groups(T, B, Hq), 256)) return NF4_ERR_UNSUPPORTED;
   const PromptArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                      q_stride, k_stride, v_stride, offsets, static_cast<int32_t>(T), B, Hq, Hkv, D, scale,
                      fill_outside != 0};
@@ -174,7 +195,7 @@ int nf4_prompt_attention_fwd(const void* q, int64_t q_stride, const void* k, int
 }
 
 size_t nf4_prompt_attention_bwd_workspace(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
-  if (check_heads(T, B, Hq, Hkv, D)) return SIZE_MAX;
+  if (check_prompt(T, B, Hq, Hkv, D, 512)) return SIZE_MAX;
   return T == 0 ? 0 : prompt_bwd_ws_bytes(T, B, Hq, Hkv, D);
 }
 
@@ -183,7 +204,7 @@ int nf4_prompt_attention_bwd(const void* grad_out, int64_t grad_stride, const vo
                              const float* lse, int64_t T, const int32_t* offsets, int32_t B, int32_t Hq, int32_t Hkv,
                              int32_t D, float scale, void* grad_q, void* grad_k, void* grad_v, int fill_outside, void* ws,
                              size_t ws_bytes, void* stream) {
-  int st = check_heads(T, B, Hq, Hkv, D);
+  int st = check_prompt(T, B, Hq, Hkv, D, 512);
   if (!st) st = check_rows(grad_out, grad_stride, T);
   if (!st) st = check_rows(q, q_stride, T);
   if (!st) st = check_rows(k, k_stride, T);
@@ -195,8 +216,6 @@ int nf4_prompt_attention_bwd(const void* grad_out, int64_t grad_stride, const vo
       !aligned(offsets, 4))
     return NF4_ERR_ALIGN;
   if (T == 0) return NF4_OK;
-  // grad_k's workgroups are of 512 threads and split the heads of a group at most to one each
-  if (!launchable(prompt_groups(T, B, Hq), 512)) return NF4_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < prompt_bwd_ws_bytes(T, B, Hq, Hkv, D)) return NF4_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return NF4_ERR_ALIGN;
   const PromptArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
