@@ -399,8 +399,19 @@ Tensor head_rows(const Tensor& t) {
                     (x.size(0) == 1 || x.stride(0) % 8 == 0) && reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0;
   return fits ? x : x.clone(at::MemoryFormat::Contiguous);
 }
+// Raises a failed C call as the package does (NF4Error with its status), from
+// autograd's thread too.
 void ok(int status, const char* name) {
-  if (status) throw std::runtime_error(std::string(name) + " failed: " + nf4_status_str(status));
+  if (!status) return;
+  const PyGILState_STATE gil = PyGILState_Ensure();
+  PyObject* lib = PyImport_ImportModule("nf4_bit_weight_amd._lib");
+  PyObject* none = lib ? PyObject_CallMethod(lib, "check", "si", name, status) : nullptr;
+  Py_XDECREF(none);
+  Py_XDECREF(lib);
+  python_error e;
+  e.persist();
+  PyGILState_Release(gil);
+  throw e;
 }
 
 // Causal attention over packed sequences, differentiable in q, k and v.  Saved

@@ -6,7 +6,9 @@ import torch
 from torch.autograd import forward_ad
 
 import attn_ref as R
+from nf4_bit_weight_amd import _lib as L
 from nf4_bit_weight_amd import nf4_prompt_attention
+from nf4_bit_weight_amd._lib import NF4Error
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +33,37 @@ def test_tangents_are_refused_in_both_directions():
         with pytest.raises(RuntimeError, match="tangent"):
             torch.autograd.grad(out, xs, forward_ad.make_dual(gy, gy), retain_graph=True)
     assert all(g.isfinite().all() for g in torch.autograd.grad(out, xs, gy))
+
+
+def many_sequences(B, heads=1024):
+    """One row in the last of B sequences, so many that the launch counts."""
+    x = R.normal(1, 1, heads, 64).to(DEV)
+    off = torch.zeros(B + 1, dtype=torch.int32, device=DEV)
+    off[-1] = 1
+    return x, off
+
+
+def test_errors_are_alike_with_and_without_gradients():
+    """What the C call refuses is an NF4Error with its status on both paths."""
+    x, off = many_sequences(16500)                             # 2^32 threads and more
+    for make in (lambda t: t, lambda t: t.clone().requires_grad_()):
+        with pytest.raises(NF4Error) as e:
+            nf4_prompt_attention(make(x), make(x), make(x), off)
+        assert e.value.status == L.NF4_ERR_UNSUPPORTED and "nf4_prompt_attention_fwd" in str(e.value)
+
+
+def test_backward_errors_carry_their_status():
+    """A saved tensor that a hook gives back misaligned is refused by the C call,
+    on autograd's thread."""
+    off = R.offsets_of([9]).to(DEV)
+
+    def shifted(t):
+        if t.dtype != torch.bfloat16:
+            return t
+        return torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)[1:].view(t.shape).copy_(t)
+    xs = leaves(9, 2, 1, 64)
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, shifted):
+        out = nf4_prompt_attention(*xs, off)
+    with pytest.raises(NF4Error) as e:
+        torch.autograd.grad(out, xs, torch.ones_like(out))
+    assert e.value.status == L.NF4_ERR_ALIGN and "nf4_prompt_attention_bwd" in str(e.value)
