@@ -424,6 +424,9 @@ struct PromptAttention : torch::autograd::Function<PromptAttention> {
                         const Tensor& offsets, double scale) {
     const Tensor q2 = head_rows(q), k2 = head_rows(k), v2 = head_rows(v);
     const Prompt p = prompt_of(q2, k2, v2, offsets, scale);
+    // refused here, not in a backward pass that cannot start
+    if (nf4_prompt_attention_bwd_workspace(p.q.T, p.B, p.q.H, p.k.H, p.D) == SIZE_MAX)
+      ok(NF4_ERR_UNSUPPORTED, "nf4_prompt_attention_bwd");
     const Tensor out = fresh({p.q.T, p.q.H, p.D}, at::kBFloat16, p.dev), rest = fresh({p.q.T, p.q.H, p.D}, at::kBFloat16, p.dev),
                  lse = fresh({p.q.H, p.q.T}, at::kFloat, p.dev);
     ok(run_forward(p, out, rest, lse, true), "nf4_prompt_attention_fwd");

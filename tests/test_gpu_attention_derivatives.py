@@ -7,7 +7,7 @@ from torch.autograd import forward_ad
 
 import attn_ref as R
 from nf4_bit_weight_amd import _lib as L
-from nf4_bit_weight_amd import nf4_prompt_attention
+from nf4_bit_weight_amd import api, nf4_prompt_attention
 from nf4_bit_weight_amd._lib import NF4Error
 
 pytestmark = pytest.mark.gpu
@@ -49,7 +49,7 @@ def test_errors_are_alike_with_and_without_gradients():
     for make in (lambda t: t, lambda t: t.clone().requires_grad_()):
         with pytest.raises(NF4Error) as e:
             nf4_prompt_attention(make(x), make(x), make(x), off)
-        assert e.value.status == L.NF4_ERR_UNSUPPORTED and "nf4_prompt_attention_fwd" in str(e.value)
+        assert e.value.status == L.NF4_ERR_UNSUPPORTED
 
 
 def test_backward_errors_carry_their_status():
@@ -67,3 +67,14 @@ def test_backward_errors_carry_their_status():
     with pytest.raises(NF4Error) as e:
         torch.autograd.grad(out, xs, torch.ones_like(out))
     assert e.value.status == L.NF4_ERR_ALIGN and "nf4_prompt_attention_bwd" in str(e.value)
+
+
+def test_sizes_that_only_the_backward_refuses_are_refused_at_once():
+    """grad_k's workgroups are twice as large: a call that records gradients must
+    not run forward into a backward pass that cannot start."""
+    x, off = many_sequences(8300)
+    api.nf4_reset_path_counts()
+    with pytest.raises(NF4Error) as e:
+        nf4_prompt_attention(x.clone().requires_grad_(), x, x, off)
+    assert e.value.status == L.NF4_ERR_UNSUPPORTED and "nf4_prompt_attention_bwd" in str(e.value)
+    assert api.nf4_path_counts()["prompt_fwd"] == 0
