@@ -391,12 +391,12 @@ PyObject* prompt_bwd(PyObject* const* a) {
 }
 
 // t [T, heads, D] as the kernels take it: bf16, the heads of a row contiguous,
-// rows 16-byte aligned.
+// rows 16-byte aligned and at most 2^24 elements apart.
 Tensor head_rows(const Tensor& t) {
   const Tensor x = t.scalar_type() == at::kBFloat16 ? t : t.to(at::kBFloat16);
   if (x.dim() != 3 || x.numel() == 0) return x;
   const bool fits = x.stride(2) == 1 && (x.size(1) == 1 || x.stride(1) == x.size(2)) &&
-                    (x.size(0) == 1 || x.stride(0) % 8 == 0) && reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0;
+                    (x.size(0) == 1 || (x.stride(0) % 8 == 0 && x.stride(0) <= 1 << 24)) && reinterpret_cast<uintptr_t>(x.data_ptr()) % 16 == 0;
   return fits ? x : x.clone(at::MemoryFormat::Contiguous);
 }
 // Raises a failed C call as the package does (NF4Error with its status), from

@@ -78,3 +78,23 @@ def test_sizes_that_only_the_backward_refuses_are_refused_at_once():
         nf4_prompt_attention(x.clone().requires_grad_(), x, x, off)
     assert e.value.status == L.NF4_ERR_UNSUPPORTED and "nf4_prompt_attention_bwd" in str(e.value)
     assert api.nf4_path_counts()["prompt_fwd"] == 0
+
+
+@pytest.mark.parametrize("grads", [False, True])
+def test_rows_too_far_apart_for_the_kernels_are_copied(grads):
+    """Any layout is taken: rows more than 2^24 elements apart as well."""
+    off = R.offsets_of([2]).to(DEV)
+    xs = [x.detach() for x in leaves(2, 2, 2, 64)]
+    gy = R.normal(9, 2, 2, 64).to(DEV)
+
+    def far(x):
+        y = torch.empty(2 ** 24 + 8 + 128, dtype=x.dtype, device=DEV).as_strided((2, 2, 64), (2 ** 24 + 8, 64, 1))
+        return y.copy_(x)
+    want = nf4_prompt_attention(*xs, off)
+    assert torch.equal(nf4_prompt_attention(*(far(x) for x in xs), off), want)
+    if grads:
+        near = [x.clone().requires_grad_() for x in xs]
+        g = torch.autograd.grad(nf4_prompt_attention(*near, off), near, gy)
+        apart = [far(x).requires_grad_() for x in xs]
+        got = torch.autograd.grad(nf4_prompt_attention(*apart, off), apart, far(gy))
+        assert all(torch.equal(a, b) for a, b in zip(got, g))
