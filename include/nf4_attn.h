@@ -25,11 +25,11 @@
  *
  * Sequences.  offsets int32 [B + 1] as in the grouped calls of nf4.h: rows
  * offsets[b] .. offsets[b+1]-1 belong to sequence b, non-decreasing, empty
- * sequences allowed (offsets that overlap or leave 0 .. T give wrong rows, but
- * no access out of range).  For the cache calls NULL means one row per sequence
- * (T == B).  Rows outside every sequence (padding behind the last one) are
- * left as they were where fill_outside is 0 and written as zeros where it is 1;
- * they are never read.
+ * sequences allowed (offsets that decrease, overlap or leave 0 .. T give
+ * wrong rows, but no access out of range).  For the cache calls NULL means one
+ * row per sequence (T == B).  Rows outside every sequence (padding behind the
+ * last one) are left as they were where fill_outside is 0 and written as zeros
+ * where it is 1; they are never read.
  *
  * Cache.  P pages of `page` tokens (a multiple of 16):
  *   codes  u8  [P, Hkv, page, D / 2]    two 4-bit patterns a byte, element 2i in
@@ -76,7 +76,8 @@ extern "C" {
  *              or (2i, 2i + 1) where interleaved != 0.  rotary is a multiple of
  *              16, at most D; 0 rotates nothing (inv_freq may then be NULL).
  *              The angle, its sine and cosine and the turn are computed in 64
- *              bits and rounded once to bf16; the cache keeps the rounded keys.
+ *              bits, rounded to fp32 and from there to bf16; the cache keeps the
+ *              rounded keys.
  *   q, q_out   NULL together: no queries.  q_out bf16 [T, Hq, D].
  *   k_out      NULL, or bf16 [T, Hkv, D]: the rotated keys.
  */

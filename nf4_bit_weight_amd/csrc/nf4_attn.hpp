@@ -69,7 +69,7 @@ hipError_t launch_kv_attention(const KVAttnPlan& pl, const KVCache& c, const KVS
                                hipStream_t stream);
 
 hipError_t launch_prompt_fwd(const PromptArgs& a, void* out, void* rest, float* lse, hipStream_t stream);
-size_t prompt_bwd_ws_bytes(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D);
+size_t prompt_bwd_ws_bytes(int64_t T, int32_t Hq, int32_t Hkv, int32_t D);
 hipError_t launch_prompt_bwd(const PromptArgs& a, const void* grad_out, int64_t grad_stride, const void* out,
                              const void* rest, const float* lse, void* grad_q, void* grad_k, void* grad_v, void* ws,
                              hipStream_t stream);

@@ -196,7 +196,7 @@ int nf4_prompt_attention_fwd(const void* q, int64_t q_stride, const void* k, int
 
 size_t nf4_prompt_attention_bwd_workspace(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
   if (check_prompt(T, B, Hq, Hkv, D, 512)) return SIZE_MAX;
-  return T == 0 ? 0 : prompt_bwd_ws_bytes(T, B, Hq, Hkv, D);
+  return T == 0 ? 0 : prompt_bwd_ws_bytes(T, Hq, Hkv, D);
 }
 
 int nf4_prompt_attention_bwd(const void* grad_out, int64_t grad_stride, const void* q, int64_t q_stride, const void* k,
@@ -216,7 +216,7 @@ int nf4_prompt_attention_bwd(const void* grad_out, int64_t grad_stride, const vo
       !aligned(offsets, 4))
     return NF4_ERR_ALIGN;
   if (T == 0) return NF4_OK;
-  if (!ws || ws_bytes < prompt_bwd_ws_bytes(T, B, Hq, Hkv, D)) return NF4_ERR_WORKSPACE;
+  if (!ws || ws_bytes < prompt_bwd_ws_bytes(T, Hq, Hkv, D)) return NF4_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return NF4_ERR_ALIGN;
   const PromptArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                      q_stride, k_stride, v_stride, offsets, static_cast<int32_t>(T), B, Hq, Hkv, D, scale,

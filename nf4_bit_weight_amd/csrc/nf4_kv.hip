@@ -229,8 +229,11 @@ constexpr int kStep = 128;           // tokens per workgroup step, 32 a wave
 // sequence, 32 heads on 8, whole and shared: 256 tokens 5.8 and 8.1 us, 512
 // tokens 7.8 and 8.2, 1024 tokens 11.9 and 8.3.
 constexpr int kSoloSteps = 4;
-// Workgroups per compute unit that share the steps, all resident at once: 2
-// (131071 tokens, before non-temporal reads: 34 us; 3 make 39, 4 make 39, 6 make 44).
+// Workgroups per compute unit that share the steps, all resident at once.  At
+// D = 128 two fit: 131071 tokens, 32 heads on 8: 37 us with 2 (the join included),
+// 42 with 3, 44 with 4; 64 sequences of up to 8192: 60, 67, 65.  At D = 64 four fit,
+// and neither side wins everywhere: 64 such sequences, 64 heads on 8: 45 us with 2,
+// 39 with 4; 131071 tokens, 8 heads on 2: 17 and 20.
 constexpr int kWorkers = 2;
 // Steps that starting and ending a unit counts as where the steps are dealt out
 // (a start takes 1.7 us, an end 1.0, a step 1.3).  64 sequences of up to 8192
@@ -468,8 +471,10 @@ __global__ __launch_bounds__(256, 2) void k_kv_attention(KVCache c, KVSeqs s, co
       }
       at += kStep;
       KVTile<D>& t = ring[slot];
-      // one row tile a sequence: nobody else reads this (131071 tokens: 31.6 us, 33.8
-      // without the hint; several row tiles lose 1 to 6 % with it)
+      // one row tile a sequence: as a rule nobody else reads this (131071 tokens: 31.6
+      // us, 33.8 without the hint; several row tiles lose 1 to 6 % with it).  Where
+      // somebody does, the hint costs nothing: 64 sequences over the same 8192 tokens
+      // 99.0 us with and without, one of 16 sequences with 33 rows 49.4 and 49.5
       constexpr bool kOnce = MT == 1;
       const uint32_t l16 = 16 * lane;
       const int64_t mine = lane < 32 ? vec[0] : vec[1];

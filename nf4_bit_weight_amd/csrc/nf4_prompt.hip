@@ -281,7 +281,7 @@ __device__ __forceinline__ int head_of(int x, int heads) { return heads % 8 == 0
 // One workgroup: 128 query rows of one head, streaming keys and values.  Bound
 // by the matrix and vector units together (a 64-key tile is 1024 cycles of
 // products and about 900 of exponentials and sums a wave, two waves a SIMD):
-// 8192 rows, 32 heads on 8 of 128: 488 to 516 us, 1065 to 1127 TFLOP/s, where this card's
+// 8192 rows, 32 heads on 8 of 128: 488 to 548 us by the card, 1003 to 1127 TFLOP/s, where this card's
 // library product of 8192 cubed reaches 1240.
 template <int D>
 __global__ __launch_bounds__(256, 2) void k_prompt_fwd(PromptArgs a, uint16_t* __restrict__ out,
@@ -816,9 +816,15 @@ int64_t tile_bound(int64_t T, int32_t B) { return T / kRows + B + 1; }
 int64_t stat_floats(int64_t T, int32_t Hq) { return (2 * T * Hq + 3) / 4 * 4; }
 
 // Workgroups over which the heads of a group are split: as many as bring the
-// launch to one workgroup per compute unit.
-int head_parts(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int cus) {
-  const int64_t tiles = (T / kRows + 1) * Hkv;                  // of one sequence; more make more
+// launch to one workgroup per compute unit, the rows counted as one sequence's
+// (lengths are on the device).  Unsplit, a small training step (5 sequences up
+// to 203 rows, 8 heads on 2 of 64) takes 42 us backward, split 26.  Many short sequences
+// have more tiles than that and gain nothing by the split (16 of 60 rows, 40 heads
+// on 8 of 128: 54 us, 39 unsplit; 64 of 8 rows, 32 heads on 8: 92 and 62); with a
+// tile counted for each sequence others lose (8 of up to 400 rows, 32 heads on 8: 75
+// us, 91 so; 40 of 200 rows, 7 heads on 1: 75 and 83).
+int head_parts(int64_t T, int32_t Hq, int32_t Hkv, int cus) {
+  const int64_t tiles = (T / kRows + 1) * Hkv;
   const int64_t want = cus / tiles;
   return static_cast<int>(want < 1 ? 1 : want > Hq / Hkv ? Hq / Hkv : want);
 }
@@ -837,7 +843,7 @@ hipError_t backward(const PromptArgs& a, const GradArgs& g, void* gq, void* gk, 
   k_prompt_bwd_q<D><<<static_cast<unsigned>(bound) * a.Hq, 256, 0, stream>>>(a, g, static_cast<uint16_t*>(gq), bound);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int parts = head_parts(a.T, a.B, a.Hq, a.Hkv, device_cu_count());
+  const int parts = head_parts(a.T, a.Hq, a.Hkv, device_cu_count());
   float* part = g.stat + stat_floats(a.T, a.Hq);
   k_prompt_bwd_kv<D><<<static_cast<unsigned>(bound) * a.Hkv * parts, 512, 0, stream>>>(
       a, g, static_cast<uint16_t*>(gk), static_cast<uint16_t*>(gv), part, parts, bound);
@@ -863,8 +869,8 @@ hipError_t launch_prompt_bwd(const PromptArgs& a, const void* grad_out, int64_t 
   return a.D == 128 ? backward<128>(a, g, grad_q, grad_k, grad_v, stream) : backward<64>(a, g, grad_q, grad_k, grad_v, stream);
 }
 
-size_t prompt_bwd_ws_bytes(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
-  const int parts = head_parts(T, B, Hq, Hkv, device_cu_count());
+size_t prompt_bwd_ws_bytes(int64_t T, int32_t Hq, int32_t Hkv, int32_t D) {
+  const int parts = head_parts(T, Hq, Hkv, device_cu_count());
   const int64_t sums = parts > 1 ? 2 * parts * T * Hkv * D : 0;
   return static_cast<size_t>(stat_floats(T, Hq) + sums) * sizeof(float);
 }
