@@ -56,7 +56,14 @@ long long integer(PyObject* o, const char* name) {
   }
   return v;
 }
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject* o, const char* name) {
+  const int t = PyObject_IsTrue(o);
+  if (t < 0) {
+    PyErr_Clear();
+    refuse(name, " must be true or false");
+  }
+  return t == 1;
+}
 
 // No call has a forward derivative: a tangent would be lost without a word.
 using Named = std::initializer_list<std::pair<const char*, PyObject*>>;
@@ -240,6 +247,7 @@ PyObject* kv_append(PyObject* const* a) {
   const Rows k = rows_of(a[4], "k", c.H, c.D, -1, c.dev), v = rows_of(a[5], "v", c.H, c.D, k.T, c.dev);
   const Seqs s = seqs_of(a[6], a[7], a[8], k.T, c.dev);
   const float* inv = nullptr;
+  const bool interleaved = truth(a[10], "interleaved");
   int64_t rotary = 0;
   if (given(a[9])) {
     const Tensor& f = tensor(a[9], "inv_freq");
@@ -260,7 +268,7 @@ PyObject* kv_append(PyObject* const* a) {
   } else if (given(a[13])) {
     refuse("q_out without q");
   }
-  if (given(a[14]) || truth(a[12])) {
+  if (truth(a[12], "return_k") || given(a[14])) {
     bool kfill;
     k_out = result(a[14], "k_out", k.T, c.H, c.D, c.dev, kfill);
     if (given(a[11]) && kfill != fill) refuse("pass both of q_out and k_out, or neither");
@@ -268,7 +276,7 @@ PyObject* kv_append(PyObject* const* a) {
   }
   const On on(c.dev);
   const int st = nf4_kv_append(q.p, q.stride, k.p, k.stride, v.p, v.stride, k.T, Hq, SEQ_ARGS(s), inv,
-                               static_cast<int32_t>(rotary), truth(a[10]), CACHE_ARGS(c), ptr(q_out), ptr(k_out), fill,
+                               static_cast<int32_t>(rotary), interleaved, CACHE_ARGS(c), ptr(q_out), ptr(k_out), fill,
                                on.stream);
   return st ? PyLong_FromLong(st) : several(q_out, k_out);
 }
@@ -370,7 +378,7 @@ PyObject* prompt_fwd(PyObject* const* a) {
   bool fill;
   const Tensor out = result(a[5], "out", p.q.T, p.q.H, p.D, p.dev, fill);
   Tensor rest, lse;
-  const bool keep = truth(a[6]);
+  const bool keep = truth(a[6], "for_backward");
   if (keep) {
     rest = fresh({p.q.T, p.q.H, p.D}, at::kBFloat16, p.dev);
     lse = fresh({p.q.H, p.q.T}, at::kFloat, p.dev);

@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import attn_ref as R
-from nf4_bit_weight_amd import (nf4_kv_append, nf4_kv_attention, nf4_kv_cache, nf4_kv_dequantize, nf4_prompt_attention)
+from nf4_bit_weight_amd import (nf4_kv_append, nf4_kv_attention, nf4_kv_cache, nf4_kv_dequantize, nf4_prompt_attention,
+                                nf4_prompt_attention_fwd)
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +106,13 @@ def test_cache_values_at_the_ends(D, rows, lens, alike, top):
         want, bound = R.attend(q[at:at + m].double(), kd, vd, seen, 1.0)
         R.within(out[at:at + m], want, bound, f"values of {top}, sequence {b}")
         at += m
+
+
+def test_flags_without_a_truth_value_are_refused():
+    cache = nf4_kv_cache(1, 1, 16, 64, DEV)
+    x = R.normal(1, 1, 1, 64).to(DEV)
+    for name in ("interleaved", "return_k"):
+        with pytest.raises(ValueError, match=name):
+            nf4_kv_append(cache, x, x, i32([1]), i32([[0]]), **{name: np.ones(2)})
+    with pytest.raises(ValueError, match="for_backward"):
+        nf4_prompt_attention_fwd(x, x, x, i32([0, 1]), for_backward=np.ones(2))
