@@ -124,7 +124,17 @@ extern "C" {
 #define NF4_PATH_KV_ATTENTION  12  /* attention over the 4-bit cache            */
 #define NF4_PATH_PROMPT_FWD    13  /* causal attention over packed prompts      */
 #define NF4_PATH_PROMPT_BWD    14  /* its backward pass                         */
-#define NF4_PATH_COUNT         15
+#define NF4_PATH_ROUTE_FWD     15  /* experts (nf4_experts.h): the choice       */
+#define NF4_PATH_ROUTE_BWD     16  /* its backward pass                         */
+#define NF4_PATH_EXPERT_PLAN   17  /* the plan of a choice                      */
+#define NF4_PATH_EXPERT_GATHER 18  /* tokens' rows to their experts' places     */
+#define NF4_PATH_EXPERT_GATHER_BWD 19
+#define NF4_PATH_EXPERT_COMBINE 20 /* experts' rows back to their tokens        */
+#define NF4_PATH_EXPERT_COMBINE_BWD 21
+#define NF4_PATH_INT8_QUANTIZE 22  /* 8-bit integers (nf4_int8.h): rows         */
+#define NF4_PATH_INT8_MATMUL   23  /* the product                               */
+#define NF4_PATH_INT8_GROUPED  24  /* the product of a stack of experts         */
+#define NF4_PATH_COUNT         25
 
 /*
  * nf4_quantize -- NF4 blockwise quantisation of w [N, K] (bitsandbytes #2034,

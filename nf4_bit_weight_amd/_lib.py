@@ -1,5 +1,5 @@
-"""ctypes loader for libnf4.so (the C ABI declared in include/nf4.h and
-include/nf4_attn.h).
+"""ctypes loader for libnf4.so (the C ABI declared in include/nf4.h,
+include/nf4_attn.h, include/nf4_experts.h and include/nf4_int8.h).
 
 The library must be built in-tree first (`python -m nf4_bit_weight_amd.build`
 or __graft_entry__.build()).  There is no fallback: if the shared library is
@@ -29,6 +29,12 @@ NF4_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 NF4_DTYPE_F32 = 0
 NF4_DTYPE_BF16 = 1
+NF4_DTYPE_I8 = 2             # rows of integers (nf4_int8.h)
+
+NF4_SCORE_SOFTMAX = 0        # nf4_experts.h
+NF4_SCORE_SIGMOID = 1
+NF4_GROUP_MAX = 0
+NF4_GROUP_TOP2 = 1
 
 NF4_OP_QUANTIZE = 0
 NF4_OP_MATMUL_FWD = 1
@@ -40,7 +46,9 @@ NF4_OP_MATMUL_BWD_INPUT_8BIT = 6
 
 PATHS = ("quantize", "dequantize", "fwd_tiled", "fwd_small_m", "bwd_tiled",
          "splitk_reduce", "grouped_fwd", "grouped_bwd", "fwd_8bit", "bwd_8bit",
-         "kv_append", "kv_dequantize", "kv_attention", "prompt_fwd", "prompt_bwd")
+         "kv_append", "kv_dequantize", "kv_attention", "prompt_fwd", "prompt_bwd",
+         "route_fwd", "route_bwd", "expert_plan", "expert_gather", "expert_gather_bwd", "expert_combine",
+         "expert_combine_bwd", "int8_quantize", "int8_matmul", "int8_grouped")
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -54,7 +62,8 @@ _f32 = ctypes.c_float
 _CACHE = [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32]   # k_codes .. v_scale, P, page, Hkv, D
 _SEQS = [_vp, _vp, _i32, _vp, _i32]                     # offsets, lengths, B, page_table, width
 
-# name -> (restype, argtypes); the full exported surface of nf4.h and nf4_attn.h
+# name -> (restype, argtypes); the full exported surface of nf4.h, nf4_attn.h, nf4_experts.h and
+# nf4_int8.h
 SIGNATURES = {
     "nf4_quantize": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _size, _vp]),
     "nf4_dequantize": (_int, [*_W, _int, _vp, _vp]),
@@ -87,6 +96,21 @@ SIGNATURES = {
     "nf4_prompt_attention_bwd": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i32, _i32,
                                         _i32, _i32, _f32, _vp, _vp, _vp, _int, _vp, _size, _vp]),
     "nf4_prompt_attention_bwd_workspace": (_size, [_i64, _i32, _i32, _i32, _i32]),
+    "nf4_route_fwd": (_int, [_vp, _int, _i64, _i64, _i32, _i32, _vp, _int, _i32, _i32, _int, _int, _f32, _vp, _vp, _vp, _vp, _vp,
+                             _vp, _size, _vp]),
+    "nf4_route_bwd": (_int, [_vp, _vp, _int, _i64, _i64, _i32, _i32, _vp, _vp, _int, _int, _f32, _vp, _vp]),
+    "nf4_expert_plan": (_int, [_vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _size, _vp]),
+    "nf4_expert_plan_workspace": (_size, [_i64, _i32, _i32]),
+    "nf4_expert_gather": (_int, [_vp, _int, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _int, _vp]),
+    "nf4_expert_gather_bwd": (_int, [_vp, _int, _i64, _i64, _i32, _vp, _vp, _vp]),
+    "nf4_expert_combine_fwd": (_int, [_vp, _int, _i64, _i64, _i32, _vp, _vp, _vp, _vp]),
+    "nf4_expert_combine_bwd": (_int, [_vp, _i64, _vp, _int, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _int, _vp]),
+    "nf4_int8_row_bytes": (_i64, [_i64]),
+    "nf4_int8_quantize": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "nf4_int8_matmul": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _int, _vp, _size, _vp]),
+    "nf4_int8_grouped_matmul": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _vp, _i32, _i64, _vp, _vp, _i64, _i64, _vp, _int, _int,
+                                       _vp, _size, _vp]),
+    "nf4_int8_workspace": (_size, [_int, _i64, _i64, _i64, _i64, _i32]),
 }
 
 _lib = None

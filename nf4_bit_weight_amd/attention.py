@@ -52,7 +52,8 @@ def _call(name: str, *args):
 
 
 _C_NAMES = {"prompt_fwd": "prompt_attention_fwd", "prompt_bwd": "prompt_attention_bwd",
-            "prompt_attention": "prompt_attention_fwd"}
+            "prompt_attention": "prompt_attention_fwd", "route": "route_fwd", "expert_combine": "expert_combine_fwd",
+            "int8_grouped": "int8_grouped_matmul"}
 
 
 @dataclass

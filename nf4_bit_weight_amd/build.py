@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libnf4.so")
 ARCH = "gfx950"
 
 SOURCES = ("nf4_abi.hip", "nf4_codec.hip", "nf4_gemm.hip", "nf4_gemv.hip", "nf4_attn_abi.hip",
-           "nf4_kv.hip", "nf4_prompt.hip")
+           "nf4_kv.hip", "nf4_prompt.hip", "nf4_experts_abi.hip", "nf4_experts.hip", "nf4_int8.hip")
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",
@@ -37,12 +37,12 @@ HIPCC_FLAGS = [
 ]
 
 
-TORCH_SOURCE = "nf4_torch.cpp"
+TORCH_SOURCES = ("nf4_torch.cpp", "nf4_torch_experts.cpp")
 TORCH_LIB = os.path.join(PKG, "_nf4_torch.so")
 
 
-def torch_module_cmds(obj: str):
-    """(compile, link) of the binding module: plain host C++."""
+def torch_module_cmds(objs):
+    """(one compile of each source, link) of the binding module: plain host C++."""
     import sysconfig
 
     import torch
@@ -50,11 +50,12 @@ def torch_module_cmds(obj: str):
     base = os.path.dirname(os.path.abspath(torch.__file__))
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     inc = [os.path.join(base, "include"), sysconfig.get_paths()["include"], os.path.join(rocm, "include")]
-    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+    compile_ = [["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
                 f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-                *[f for d in inc for f in ("-isystem", d)], "-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj]
+                *[f for d in inc for f in ("-isystem", d)], "-c", os.path.join(CSRC, src), "-o", obj]
+                for src, obj in zip(TORCH_SOURCES, objs)]
     lib = os.path.join(base, "lib")
-    link = ["g++", "-shared", "-fPIC", obj, "-L", PKG, "-l:libnf4.so", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+    link = ["g++", "-shared", "-fPIC", *objs, "-L", PKG, "-l:libnf4.so", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
             "-lc10_hip", "-Wl,-rpath,$ORIGIN", "-o", TORCH_LIB + ".tmp"]
     return compile_, link
 
@@ -81,9 +82,9 @@ def build(verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    torch_obj = os.path.join(BUILD_DIR, TORCH_SOURCE.replace(".cpp", ".o"))
-    torch_compile, torch_link = torch_module_cmds(torch_obj)
-    procs.append((TORCH_SOURCE, subprocess.Popen(torch_compile, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    torch_compile, torch_link = torch_module_cmds([os.path.join(BUILD_DIR, s.replace(".cpp", ".o")) for s in TORCH_SOURCES])
+    for src, cmd in zip(TORCH_SOURCES, torch_compile):
+        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
