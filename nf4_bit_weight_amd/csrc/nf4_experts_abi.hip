@@ -50,7 +50,7 @@ int check_int8(int x_dtype, int64_t x_rows, int64_t M, int64_t N, int64_t K, int
   if (x_rows < 0 || M < 0 || N < 0 || K < 0 || E < 0) return NF4_ERR_SHAPE;
   if (K > 130944 || x_rows > 1 << 28 || M > 1 << 28 || N > 1 << 28 || E > 1024) return NF4_ERR_UNSUPPORTED;
   if (!launchable(x_rows, 256)) return NF4_ERR_UNSUPPORTED;
-  if (!launchable((N + 15) / 16 * (M / 16 + E + 1), 256)) return NF4_ERR_UNSUPPORTED;
+  if (!int8_launchable(M, N, E)) return NF4_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return NF4_OK;
   if (x_dtype != NF4_DTYPE_I8) {
     pl.q = static_cast<size_t>(x_rows) * int8_row_bytes(K);
@@ -80,6 +80,8 @@ int int8_product(const void* x, int x_dtype, int64_t stride, const float* x_scal
   const hipStream_t s = static_cast<hipStream_t>(stream);
   Int8Args a{static_cast<const int8_t*>(x), x_scale, x_rows, tokens, offsets, E, M, N, int8_row_bytes(K), q, scale, bias, y,
              y_dtype == NF4_DTYPE_BF16, fill != 0};
+  const Int8Source source{x, x_dtype == NF4_DTYPE_BF16, stride, static_cast<int32_t>(K)};
+  if (!ready && int8_fused(a)) return to_status(launch_int8_matmul(a, &source, s));
   if (!ready) {
     int8_t* xq = static_cast<int8_t*>(ws);
     float* xs = reinterpret_cast<float*>(xq + pl.q);
@@ -90,7 +92,7 @@ int int8_product(const void* x, int x_dtype, int64_t stride, const float* x_scal
     a.x = xq;
     a.x_scale = xs;
   }
-  return to_status(launch_int8_matmul(a, s));
+  return to_status(launch_int8_matmul(a, nullptr, s));
 }
 
 }  // namespace

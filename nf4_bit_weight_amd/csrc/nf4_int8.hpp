@@ -26,6 +26,16 @@ struct Int8Args {
 
 hipError_t launch_int8_quantize(const void* x, bool bf16, int64_t stride, int64_t M, int64_t K, int8_t* q, float* scale,
                                 hipStream_t stream);
-hipError_t launch_int8_matmul(const Int8Args& a, hipStream_t stream);
+// x before it is quantised
+struct Int8Source {
+  const void* x;
+  bool bf16;
+  int64_t stride;
+  int32_t K;
+};
+bool int8_launchable(int64_t M, int64_t N, int32_t E);
+// Whether the product quantises x itself (source given; a.x and a.x_scale are not read).
+bool int8_fused(const Int8Args& a);
+hipError_t launch_int8_matmul(const Int8Args& a, const Int8Source* source, hipStream_t stream);
 
 }  // namespace nf4

@@ -156,7 +156,7 @@ def quantize(x):
 
 def product(q, s, w, sw, bias=None):
     """(y float64 of exact sums, bound of the fp32 steps: the sum's rounding, two products, the bias)."""
-    y = (q @ w.T).double() * sw.double() * s.double()[:, None]
+    y = (q.double() @ w.double().T) * sw.double() * s.double()[:, None]      # (integers below 2^53: exact)
     size = y.abs()
     if bias is not None:
         y, size = y + bias.double(), size + bias.double().abs()

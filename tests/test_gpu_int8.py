@@ -67,7 +67,12 @@ def test_quantize_edges(dtype):
 
 SHAPES = [(1, 1, 1), (1, 16, 64), (1, 4096, 4096), (2, 100, 300), (3, 33, 128), (8, 1000, 640), (16, 129, 4096), (17, 64, 200), (31, 500, 1024),
           (32, 1024, 2048), (33, 77, 129), (64, 256, 512), (65, 300, 384), (100, 1024, 1152), (128, 128, 4096), (129, 257, 640),
-          (200, 4096, 256), (256, 256, 128), (300, 513, 5120), (512, 1024, 1024), (700, 1000, 777), (1024, 2048, 512), (2048, 640, 896)]
+          (200, 4096, 256), (256, 256, 128), (300, 513, 5120), (512, 1024, 1024), (700, 1000, 777), (1024, 2048, 512), (2048, 640, 896),
+          # every shape of tile, whole and with parts; K of one step, of fewer than are in flight, of more
+          (512, 4096, 128), (1000, 4100, 500), (1024, 4096, 640), (520, 4000, 1000), (2048, 4096, 128), (2048, 4000, 300),
+          (4096, 4096, 256), (2500, 3500, 700),
+          # few rows: channels 16, 32 and 64 a workgroup, K in one to eight parts and beyond what is in flight
+          (5, 14336, 128), (16, 7300, 384), (1, 15000, 600), (20, 4096, 1300), (33, 8100, 2200), (50, 1000, 8000), (64, 4096, 200), (2, 40, 20000)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -153,7 +158,8 @@ def grouped_case(seed, T, E, k, N, K, empty, dtype=torch.float32):
 
 
 GROUPED = [(1, 4, 2, 16, 64, 0), (3, 64, 8, 128, 256, 0), (5, 8, 1, 33, 100, 2), (40, 4, 2, 96, 384, 0), (64, 64, 8, 64, 128, 5), (200, 3, 1, 130, 640, 0),
-           (130, 5, 2, 256, 512, 129), (300, 8, 2, 512, 256, 1), (257, 16, 4, 1024, 128, 0), (90, 60, 4, 40, 200, 3), (20, 200, 3, 8, 64, 0), (7, 4, 2, 64, 64, 7)]
+           (130, 5, 2, 256, 512, 129), (300, 8, 2, 512, 256, 1), (257, 16, 4, 1024, 128, 0), (90, 60, 4, 40, 200, 3), (20, 200, 3, 8, 64, 0), (7, 4, 2, 64, 64, 7),
+           (1500, 4, 2, 1000, 256, 10), (3000, 4, 2, 2000, 100, 0), (2100, 5, 1, 4000, 128, 100), (900, 1, 1, 300, 384, 0)]
 
 
 @pytest.mark.parametrize("T,E,k,N,K,empty", GROUPED)
