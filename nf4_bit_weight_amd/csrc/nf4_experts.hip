@@ -2,6 +2,7 @@
 // experts' places (nf4_experts.h).
 #include <cmath>
 
+#include "nf4_attn.hpp"
 #include "nf4_device.hpp"
 #include "nf4_experts.hpp"
 #include "nf4_internal.hpp"
@@ -36,10 +37,67 @@ __device__ __forceinline__ uint32_t rank32(float x) {
   const uint32_t u = x == 0.0f ? 0u : __builtin_bit_cast(uint32_t, x);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ float number32(uint32_t r) {       // and back
+  return __builtin_bit_cast(float, r & 0x80000000u ? r & 0x7FFFFFFFu : ~r);
+}
 __device__ __forceinline__ uint64_t rank64(double x) {
   if (x != x) return ~uint64_t{0};
   const uint64_t u = x == 0.0 ? 0u : __builtin_bit_cast(uint64_t, x);
   return u >> 63 ? ~u : u | uint64_t{1} << 63;
+}
+
+// This lane's value and the one of the lane M further in a butterfly over equal
+// values: all M lanes of a block already hold the same, so a mirrored block serves as
+// well as a crossed one.  In the vector unit's lane moves (swap16, swap32: one of the two is
+// this lane's), a few cycles where a shuffle through LDS takes a hundred.
+template <int M>
+__device__ __forceinline__ void both(uint32_t v, uint32_t& x, uint32_t& y) {
+  static_assert(M == 1 || M == 2 || M == 4 || M == 8 || M == 16 || M == 32, "lanes of a block");
+  if constexpr (M <= 8) {
+    constexpr int kMove = M == 1 ? 0xB1 : M == 2 ? 0x4E : M == 4 ? 0x141 : 0x140;      // quad_perm, row_half_mirror, row_mirror
+    x = v;
+    y = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), kMove, 0xF, 0xF, true));
+  } else {
+    const float f = __builtin_bit_cast(float, v);
+    const f32x2_t p = M == 16 ? swap16(f) : swap32(f);
+    const float p0 = p[0], p1 = p[1];
+    x = __builtin_bit_cast(uint32_t, p0);
+    y = __builtin_bit_cast(uint32_t, p1);
+  }
+}
+template <int M>
+__device__ __forceinline__ void both(float v, float& x, float& y) {
+  uint32_t a, b;
+  both<M>(__builtin_bit_cast(uint32_t, v), a, b);
+  x = __builtin_bit_cast(float, a);
+  y = __builtin_bit_cast(float, b);
+}
+template <int M>
+__device__ __forceinline__ void both(uint64_t v, uint64_t& x, uint64_t& y) {
+  uint32_t a[2], b[2];
+  both<M>(static_cast<uint32_t>(v), a[0], b[0]);
+  both<M>(static_cast<uint32_t>(v >> 32), a[1], b[1]);
+  x = static_cast<uint64_t>(a[1]) << 32 | a[0];
+  y = static_cast<uint64_t>(b[1]) << 32 | b[0];
+}
+template <int M>
+__device__ __forceinline__ void both(double v, double& x, double& y) {
+  uint64_t a, b;
+  both<M>(__builtin_bit_cast(uint64_t, v), a, b);
+  x = __builtin_bit_cast(double, a);
+  y = __builtin_bit_cast(double, b);
+}
+
+// f over the L lanes of a token, the same in all of them
+template <int L, int M = 1, typename V, typename F>
+__device__ __forceinline__ V across(V v, F f) {
+  if constexpr (M < L) {
+    V x, y;
+    both<M>(v, x, y);
+    return across<L, 2 * M>(f(x, y), f);
+  } else {
+    return v;
+  }
 }
 
 // An expert in the running.  Where 32 bits order the scores, their rank and the
@@ -51,15 +109,13 @@ struct Cand<false> {
   uint64_t key;
   __device__ __forceinline__ bool over(const Cand& o) const { return key > o.key; }
   __device__ __forceinline__ int index() const { return static_cast<int>(~static_cast<uint32_t>(key)); }
-  __device__ __forceinline__ Cand from(int mask) const { return {__shfl_xor(key, mask, 64)}; }
 };
 template <>
 struct Cand<true> {
   uint64_t key;
-  int idx;
+  uint32_t idx;
   __device__ __forceinline__ bool over(const Cand& o) const { return key > o.key || (key == o.key && idx < o.idx); }
-  __device__ __forceinline__ int index() const { return idx; }
-  __device__ __forceinline__ Cand from(int mask) const { return {__shfl_xor(key, mask, 64), __shfl_xor(idx, mask, 64)}; }
+  __device__ __forceinline__ int index() const { return static_cast<int>(idx); }
 };
 
 template <int PER, bool WIDE>
@@ -83,15 +139,153 @@ __device__ __forceinline__ void sort_descending(Cand<WIDE> (&v)[PER]) {
         }
 }
 
-template <int L, typename V, typename F>
-__device__ __forceinline__ V across(V v, F f) {
-#pragma unroll
-  for (int m = 1; m < L; m <<= 1) v = f(v, __shfl_xor(v, m, 64));
-  return v;
+// e^x in 64 bits: x = n ln 2 + r, the series of e^r to its 13th term (the next is below
+// 2^-57 at |r| = ln 2 / 2), times 2^n.  Half of what the library's takes, which
+// serves the ends of the range; here they are cut off at +-700.
+__device__ __forceinline__ double exp64(double x) {
+  const double y = fmin(fmax(x, -700.0), 700.0);
+  const double n = rint(y * 1.4426950408889634074);
+  double r = fma(-n, 0.69314718055994530942, y);
+  r = fma(-n, 2.3190468138462995e-17, r);                      // ln 2 less its 64-bit value
+  double p = 1.0 / 6227020800.0;
+  p = fma(p, r, 1.0 / 479001600.0);
+  p = fma(p, r, 1.0 / 39916800.0);
+  p = fma(p, r, 1.0 / 3628800.0);
+  p = fma(p, r, 1.0 / 362880.0);
+  p = fma(p, r, 1.0 / 40320.0);
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return x != x ? x : ldexp(p, static_cast<int>(n));
+}
+// 1 / x for 1 <= x < 2^1012: the hardware's guess, made good twice
+__device__ __forceinline__ double reciprocal64(double x) {
+  double r = __builtin_amdgcn_rcp(x);
+  r = fma(fma(-x, r, 1.0), r, r);
+  return fma(fma(-x, r, 1.0), r, r);
 }
 
 // e^(l - top) as the softmax takes it: nothing for an expert that is masked out
 __device__ __forceinline__ float exp_from(float l, float top) { return l == -INFINITY ? 0.0f : expf(l - top); }
+
+// This lane's choice (-1: none), the lanes of its wave with the same expert below it, and
+// the wave's counts in s_held [waves][E]: the lanes of an expert are found by one ballot for each
+// bit of its number.  No count depends on who comes first.
+struct Claim {
+  int expert;
+  int below;
+  bool some;
+};
+__device__ __forceinline__ Claim claim(int e, int32_t E, int32_t* s_held) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  for (int x = threadIdx.x; x < waves * E; x += blockDim.x) s_held[x] = 0;
+  const bool some = static_cast<uint32_t>(e) < static_cast<uint32_t>(E);
+  uint64_t same = __ballot(some);
+  for (int bit = 1; bit < E; bit <<= 1) {
+    const uint64_t set = __ballot((e & bit) != 0);
+    same &= (e & bit) != 0 ? set : ~set;
+  }
+  const int below = __popcll(same & ((uint64_t{1} << lane) - 1));
+  __syncthreads();
+  if (some && below == 0) s_held[wave * E + e] = __popcll(same);
+  __syncthreads();
+  return {e, below, some};
+}
+// s_held to the sums over earlier waves behind `at`; all of it comes back.
+__device__ __forceinline__ int32_t sum_waves(int32_t* s_held, int32_t E, int e, int32_t at) {
+  const int waves = blockDim.x >> 6;
+  for (int w0 = 0; w0 < waves; w0 += 8) {
+    int32_t n[8];
+#pragma unroll
+    for (int w = 0; w < 8; ++w) n[w] = w0 + w < waves ? s_held[(w0 + w) * E + e] : 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      if (w0 + w < waves) s_held[(w0 + w) * E + e] = at;
+      at += n[w];
+    }
+  }
+  return at;
+}
+__device__ __forceinline__ void settle(const PlanArgs& a, const Claim& c, int32_t row, uint32_t at) {
+  if (c.some) a.tokens[row] = static_cast<int32_t>(at / static_cast<uint32_t>(a.k));
+  a.slots[at] = c.some ? row : -1;
+}
+
+// Rows of the choices [0, n) of `choices` (in LDS or memory) behind s_base, by expert
+// and then in order, a workgroup's threads of them at a time; e is this thread's first one.
+__device__ __forceinline__ void place(const PlanArgs& a, const int32_t* choices, int e, int n, uint32_t first, int32_t* s_base, int32_t* s_held) {
+  const int wave = threadIdx.x >> 6, threads = blockDim.x;
+  for (int c = 0; c < n; c += threads) {
+    const int i = c + threadIdx.x;
+    if (c > 0) e = i < n ? choices[i] : -1;
+    const Claim mine = claim(e, a.E, s_held);
+    for (int x = threadIdx.x; x < a.E; x += threads) s_base[x] = sum_waves(s_held, a.E, x, s_base[x]);
+    __syncthreads();
+    if (i < n) settle(a, mine, mine.some ? s_held[wave * a.E + mine.expert] + mine.below : -1, first + i);
+    if (c + threads < n) __syncthreads();
+  }
+}
+
+// s_first [E + 1] from the experts' counts s_count [E], by the first wave
+__device__ __forceinline__ void first_rows(const int32_t* s_count, int32_t E, int32_t* s_first) {
+  const int lane = threadIdx.x;
+  int32_t sum = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    const int32_t n = e < E ? s_count[e] : 0, incl = wave_scan(n);
+    if (e < E) s_first[e] = sum + incl - n;
+    sum += __builtin_amdgcn_readlane(incl, 63);
+  }
+  if (lane == 0) s_first[E] = sum;
+}
+
+// The counts of s_pick's choices [0, n) in s_count [E] (integers: in any order)
+__device__ __forceinline__ void count_choices(const int32_t* s_pick, int n, int32_t E, int32_t* s_count) {
+  for (int e = threadIdx.x; e < E; e += blockDim.x) s_count[e] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int e = s_pick[i];
+    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(E)) atomicAdd(&s_count[e], 1);
+  }
+  __syncthreads();
+}
+
+// The run of a workgroup: an `only` run is placed at once, else its counts go to held.
+__device__ __forceinline__ void plan_run(const PlanArgs& a, bool only, const int32_t* s_pick, int n, uint32_t first, uint16_t* held, int pitch,
+                                         int32_t* s_count, int32_t* s_first, int32_t* s_held) {
+  const int threads = blockDim.x;
+  const bool once = only && n <= threads;                      // a choice a thread: counted and placed in one pass
+  Claim mine{};
+  if (once) {
+    mine = claim(threadIdx.x < n ? s_pick[threadIdx.x] : -1, a.E, s_held);
+    for (int e = threadIdx.x; e < a.E; e += threads) s_count[e] = sum_waves(s_held, a.E, e, 0);
+    __syncthreads();
+  } else {
+    count_choices(s_pick, n, a.E, s_count);
+  }
+  if (!only) {
+    uint16_t* mine_held = held + static_cast<int64_t>(blockIdx.x) * pitch;      // (a run has at most 8192 choices)
+    for (int e = threadIdx.x; e < pitch; e += threads) mine_held[e] = e < a.E ? static_cast<uint16_t>(s_count[e]) : 0;
+    return;
+  }
+  if (threadIdx.x < 64) first_rows(s_count, a.E, s_first);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= a.E; e += threads) a.offsets[e] = s_first[e];
+  const int32_t end = s_first[a.E];
+  for (int r = end + threadIdx.x; r < n; r += threads) a.tokens[r] = -1;      // rows that belong to nobody
+  if (once) {
+    if (threadIdx.x < n)
+      settle(a, mine, mine.some ? s_first[mine.expert] + s_held[(threadIdx.x >> 6) * a.E + mine.expert] + mine.below : -1, first + threadIdx.x);
+    return;
+  }
+  __syncthreads();
+  place(a, s_pick, threadIdx.x < n ? s_pick[threadIdx.x] : -1, n, first, s_first, s_held);
+}
 
 // L lanes of a wave share a token, each holds PER neighbouring experts in
 // registers.  Each sorts its own; then k times the best of the L heads is taken
@@ -100,23 +294,23 @@ __device__ __forceinline__ float exp_from(float l, float top) { return l == -INF
 //
 // Sums are fp32.  WIDE: what the choice compares (s + bias, sums of two) is computed
 // in 64 bits, since 8191 x 256 scores hold several pairs that fp32 rounding would turn round.
+//
+// A workgroup's tokens are a run of the plan: it counts their choices for k_plan_place, or,
+// as the only one, places them itself (one launch for a batch of new tokens).
 template <typename T, int PER, int L, bool WIDE>
-__global__ __launch_bounds__(PER == 16 ? 128 : 256) void k_route(RouteArgs a) {
-  constexpr int kWaves = PER == 16 ? 2 : 4, kHeld = 64 * PER, kTokens = 64 / L, kOf = L * PER;
+__global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint16_t* held, int pitch) {
+  constexpr int kTokens = 64 / L, kOf = L * PER;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int sub = lane & (L - 1), tk = lane / L, e0 = sub * PER;
-  const bool grouped = a.groups > 1;
-  char* mine = lds + wave * kHeld * (grouped ? 24 : 8);
-  float* s_logit = reinterpret_cast<float*>(mine) + tk * kOf;                         // the token's logits
-  int32_t* s_pick = reinterpret_cast<int32_t*>(mine + kHeld * 4) + tk * kOf;          // its choice
-  uint64_t* s_score = reinterpret_cast<uint64_t*>(mine + kHeld * 8) + tk * kOf;       // what the groups are judged by
-  uint64_t* s_group = reinterpret_cast<uint64_t*>(mine + kHeld * 16) + tk * kOf;      // and the judgement
-  const int64_t t = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kTokens + tk;
+  int32_t* s_all = reinterpret_cast<int32_t*>(lds);             // the choices of the workgroup
+  int32_t* s_pick = s_all + (wave * kTokens + tk) * a.k;        // of the token
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * waves * kTokens, t = t0 + wave * kTokens + tk;
   const bool on = t < a.T;
 
   float l[PER];
-  const T* row = static_cast<const T*>(a.logits) + (on ? t * a.stride : 0) + e0;
+  const T* logits = static_cast<const T*>(a.logits) + (on ? t * a.stride : 0);
+  const T* row = logits + e0;
   constexpr int kVec = 16 / sizeof(T);                                                 // of one load
   if (a.E % kVec == 0 && a.stride % kVec == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0) {
 #pragma unroll
@@ -125,16 +319,12 @@ __global__ __launch_bounds__(PER == 16 ? 128 : 256) void k_route(RouteArgs a) {
       const bool in = on && e0 + i < a.E;
       if (in) v = *reinterpret_cast<const u32x4_t*>(row + i);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        l[i + j] = in ? element<T>(v, j) : -INFINITY;
-      }
+      for (int j = 0; j < kVec; ++j) l[i + j] = in ? element<T>(v, j) : -INFINITY;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < PER; ++i) l[i] = on && e0 + i < a.E ? value(row + i) : -INFINITY;
   }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) s_logit[e0 + i] = l[i];
 
   float top = -INFINITY;
 #pragma unroll
@@ -151,19 +341,19 @@ __global__ __launch_bounds__(PER == 16 ? 128 : 256) void k_route(RouteArgs a) {
       double sum = 0.0;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        c[i] = l[i] == -INFINITY ? 0.0 : exp(static_cast<double>(l[i]) - static_cast<double>(top));
+        c[i] = l[i] == -INFINITY ? 0.0 : exp64(static_cast<double>(l[i]) - static_cast<double>(top));
         sum += c[i];
       }
       sum = across<L>(sum, [](double x, double y) { return x + y; });
-      part = sum;
+      part = sum > 0.0 ? 1.0 / sum : sum;                      // (no expert at all: 0)
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      c[i] = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l[i]))) : c[i] / part;
+      c[i] = a.sigmoid ? reciprocal64(1.0 + exp64(-static_cast<double>(l[i]))) : c[i] * part;
       if (a.bias && e0 + i < a.E) c[i] += static_cast<double>(a.bias[e0 + i]);
       const bool live = l[i] != -INFINITY && c[i] != -INFINITY;
       if (!live) c[i] = -INFINITY;
-      v[i] = {live ? rank64(a.bias ? c[i] : static_cast<double>(l[i])) : 0, e0 + i};
+      v[i] = {live ? rank64(a.bias ? c[i] : static_cast<double>(l[i])) : 0, static_cast<uint32_t>(e0 + i)};
     }
   } else {
 #pragma unroll
@@ -171,59 +361,127 @@ __global__ __launch_bounds__(PER == 16 ? 128 : 256) void k_route(RouteArgs a) {
       v[i] = {l[i] == -INFINITY ? 0 : static_cast<uint64_t>(rank32(l[i])) << 32 | static_cast<uint32_t>(~(e0 + i))};
   }
 
-  if (grouped) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if constexpr (WIDE) s_score[e0 + i] = a.top2 ? __builtin_bit_cast(uint64_t, c[i]) : v[i].key;
-      else s_score[e0 + i] = v[i].key >> 32;
-    }
-    wave_sync();
+  if (a.groups > 1) {
     const int size = a.E / a.groups;
-    for (int g = sub; g < a.groups; g += L) {
-      const uint64_t* s = s_score + g * size;
+    auto judge = [](double one, double two, bool nan) {
+      return nan ? ~uint64_t{0} : one == -INFINITY ? 0 : rank64(two == -INFINITY ? one : one + two);
+    };
+    if (a.lanes > 0) {
+      // a group is a run of `lanes` lanes, a power of two
       uint64_t key = 0;
       if (WIDE && a.top2) {
         double one = -INFINITY, two = -INFINITY;
-        bool nan = false;
-        for (int i = 0; i < size; ++i) {
-          const double x = __builtin_bit_cast(double, s[i]);
-          nan |= x != x;
-          two = fmax(two, fmin(one, x));
-          one = fmax(one, x);
-        }
-        key = nan ? ~uint64_t{0} : one == -INFINITY ? 0 : rank64(two == -INFINITY ? one : one + two);
-      } else {
-        for (int i = 0; i < size; ++i) key = s[i] > key ? s[i] : key;
-      }
-      s_group[g] = key;
-    }
-    wave_sync();
-    for (int g = sub; g < a.groups; g += L) {
-      const uint64_t key = s_group[g];
-      int before = 0;
-      for (int o = 0; o < a.groups; ++o) before += s_group[o] > key || (s_group[o] == key && o < g);
-      s_score[g] = before < a.top_groups;
-    }
-    wave_sync();
-    int g = e0 / size, r = e0 - g * size;
+        uint32_t nan = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (e0 + i < a.E && !s_score[g]) v[i].key = 0;
-      if (++r == size) r = 0, ++g;
+        for (int i = 0; i < PER; ++i) {
+          nan |= c[WIDE ? i : 0] != c[WIDE ? i : 0];
+          two = fmax(two, fmin(one, c[WIDE ? i : 0]));
+          one = fmax(one, c[WIDE ? i : 0]);
+        }
+        auto merge = [&](auto m) {
+          if (m >= L || m >= a.lanes) return;
+          double x1, y1, x2, y2;
+          uint32_t xn, yn;
+          both<m>(one, x1, y1);
+          both<m>(two, x2, y2);
+          both<m>(nan, xn, yn);
+          one = fmax(x1, y1);
+          two = fmax(fmin(x1, y1), fmax(x2, y2));
+          nan = xn | yn;
+        };
+        merge(std::integral_constant<int, 1>{});
+        merge(std::integral_constant<int, 2>{});
+        merge(std::integral_constant<int, 4>{});
+        merge(std::integral_constant<int, 8>{});
+        merge(std::integral_constant<int, 16>{});
+        key = judge(one, two, nan != 0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const uint64_t x = WIDE ? v[i].key : v[i].key >> 32;
+          key = x > key ? x : key;
+        }
+        auto merge = [&](auto m) {
+          if (m >= L || m >= a.lanes) return;
+          uint64_t x, y;
+          both<m>(key, x, y);
+          key = x > y ? x : y;
+        };
+        merge(std::integral_constant<int, 1>{});
+        merge(std::integral_constant<int, 2>{});
+        merge(std::integral_constant<int, 4>{});
+        merge(std::integral_constant<int, 8>{});
+        merge(std::integral_constant<int, 16>{});
+      }
+      const int mine = sub / a.lanes;
+      int before = 0;
+      for (int g = 0; g < a.groups; ++g) {
+        const uint64_t other = __shfl(key, tk * L + g * a.lanes, 64);
+        before += other > key || (other == key && g < mine);
+      }
+      if (before >= a.top_groups) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) v[i].key = 0;
+      }
+    } else {
+      // any size: through LDS
+      uint64_t* s_score = reinterpret_cast<uint64_t*>(lds + a.group_lds) + (wave * kTokens + tk) * 2 * kOf;
+      uint64_t* s_group = s_score + kOf;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if constexpr (WIDE) s_score[e0 + i] = a.top2 ? __builtin_bit_cast(uint64_t, c[i]) : v[i].key;
+        else s_score[e0 + i] = v[i].key >> 32;
+      }
+      wave_sync();
+      for (int g = sub; g < a.groups; g += L) {
+        const uint64_t* s = s_score + g * size;
+        uint64_t key = 0;
+        if (WIDE && a.top2) {
+          double one = -INFINITY, two = -INFINITY;
+          bool nan = false;
+          for (int i = 0; i < size; ++i) {
+            const double x = __builtin_bit_cast(double, s[i]);
+            nan |= x != x;
+            two = fmax(two, fmin(one, x));
+            one = fmax(one, x);
+          }
+          key = judge(one, two, nan);
+        } else {
+          for (int i = 0; i < size; ++i) key = s[i] > key ? s[i] : key;
+        }
+        s_group[g] = key;
+      }
+      wave_sync();
+      for (int g = sub; g < a.groups; g += L) {
+        const uint64_t key = s_group[g];
+        int before = 0;
+        for (int o = 0; o < a.groups; ++o) before += s_group[o] > key || (s_group[o] == key && o < g);
+        s_score[g] = before < a.top_groups;
+      }
+      wave_sync();
+      int g = e0 / size, r = e0 - g * size;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (e0 + i < a.E && !s_score[g]) v[i].key = 0;
+        if (++r == size) r = 0, ++g;
+      }
     }
   }
 
   sort_descending(v);
+  uint64_t taken = 0;                                           // the key of choice `sub`
   for (int j = 0; j < a.k; ++j) {
-    Cand<WIDE> best = v[0];
-#pragma unroll
-    for (int m = 1; m < L; m <<= 1) {
-      const Cand<WIDE> o = best.from(m);
-      best = o.over(best) ? o : best;
+    const uint64_t best = across<L>(v[0].key, [](uint64_t x, uint64_t y) { return x > y ? x : y; });
+    if (j == sub) taken = best;
+    bool here = best != 0 && v[0].key == best;
+    if constexpr (WIDE && L > 1) {
+      // the lowest of the lanes that hold it: theirs are the lower experts
+      const uint64_t held = __ballot(here) >> (tk * L);
+      here = here && __ffsll(static_cast<long long>(held)) - 1 == sub;
     }
-    const bool some = best.key != 0;
-    if (sub == 0) s_pick[j] = some ? best.index() : -1;
-    if (some && best.index() / PER == sub) {
+    if (here) s_pick[j] = v[0].index();
+    if (sub == 0 && on && best == 0) s_pick[j] = -1;
+    if (here) {
 #pragma unroll
       for (int i = 0; i + 1 < PER; ++i) v[i] = v[i + 1];
       v[PER - 1].key = 0;
@@ -234,30 +492,42 @@ __global__ __launch_bounds__(PER == 16 ? 128 : 256) void k_route(RouteArgs a) {
   // Weights.  Renormalised ones are formed from the chosen alone, so that they do not
   // vanish with the scores: softmax from the largest chosen logit, sigmoid (e^l / (1 + e^l)
   // below zero) with all of them scaled up by the best where that is far down.
+  const int mine = on ? a.k : 0;
+  auto chosen = [&](int j) {                                    // the logit of a choice
+    const int e = s_pick[j];
+    if (e < 0) return -INFINITY;
+    return !WIDE && j == sub ? number32(static_cast<uint32_t>(taken >> 32)) : value(logits + e);
+  };
   float best = -INFINITY, total = 0.0f;
-  for (int j = sub; j < a.k; j += L) best = s_pick[j] >= 0 ? fmaxf(best, s_logit[s_pick[j]]) : best;
-  best = across<L>(best, [](float x, float y) { return fmaxf(x, y); });
-  if (best == -INFINITY || (a.sigmoid && best > 0.0f)) best = 0.0f;
-  if (!a.sigmoid && !a.renorm) best = top;
-  if (a.sigmoid && !a.renorm) best = 0.0f;
+  if (a.renorm) {
+    for (int j = sub; j < mine; j += L) best = fmaxf(best, chosen(j));
+    best = across<L>(best, [](float x, float y) { return fmaxf(x, y); });
+    if (best == -INFINITY || (a.sigmoid && best > 0.0f)) best = 0.0f;
+  } else {
+    best = a.sigmoid ? 0.0f : top;
+  }
   auto score = [&](float x) {
     if (!a.sigmoid) return expf(x - best);
     return x >= 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x - best) / (1.0f + expf(x));
   };
   if (a.renorm) {
-    for (int j = sub; j < a.k; j += L) total += s_pick[j] >= 0 ? score(s_logit[s_pick[j]]) : 0.0f;
+    for (int j = sub; j < mine; j += L) total += s_pick[j] >= 0 ? score(chosen(j)) : 0.0f;
   } else if (!a.sigmoid) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) total += exp_from(l[i], top);
   }
   total = across<L>(total, [](float x, float y) { return x + y; });
   if (a.sigmoid && !a.renorm) total = 1.0f;
-  if (!on) return;
-  for (int j = sub; j < a.k; j += L) {
+  for (int j = sub; j < mine; j += L) {
     const int e = s_pick[j];
     a.experts[t * a.k + j] = e;
-    a.weights[t * a.k + j] = e >= 0 ? a.scale * (score(s_logit[e]) / total) : 0.0f;
+    a.weights[t * a.k + j] = e >= 0 ? a.scale * (score(chosen(j)) / total) : 0.0f;
   }
+  if (!plan.offsets) return;
+  __syncthreads();
+  const int n = static_cast<int>(min(static_cast<int64_t>(waves * kTokens), a.T - t0)) * a.k;
+  int32_t* s_count = reinterpret_cast<int32_t*>(lds + a.plan_lds);
+  plan_run(plan, gridDim.x == 1, s_all, n, static_cast<uint32_t>(t0 * a.k), held, pitch, s_count, s_count + a.E, s_count + 2 * a.E + 1);
 }
 
 // grad_logits, with D = sum_j g_j w_j over the chosen:
@@ -343,83 +613,134 @@ hipError_t with_lanes(int32_t E, F f) {
 
 // ---- the plan --------------------------------------------------------------------
 
-// Counting sort of the choices by expert, in three steps: each workgroup counts
-// its kPairs-sized run of choices, the counts are summed over the runs, and each
-// choice finds its row: the rows of its expert in earlier runs, and those before
-// it in its own, from bit masks (one bit a choice, one mask an expert), so that
-// the order is the tokens' and no count depends on who comes first.
-// A run is 1024 choices, fewer above 256 experts: the masks take E / 8 bytes a choice, 32 KB.
-constexpr int plan_pairs(int32_t E) { return E <= 256 ? 1024 : E <= 512 ? 512 : 256; }
-int64_t plan_runs(int64_t pairs, int32_t E) { return (pairs + plan_pairs(E) - 1) / plan_pairs(E); }
-
-__global__ __launch_bounds__(256) void k_plan_count(PlanArgs a, int pairs, int32_t* held) {
-  extern __shared__ int32_t s_held[];
-  for (int e = threadIdx.x; e < a.E; e += 256) s_held[e] = 0;
-  __syncthreads();
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * pairs, all = static_cast<int64_t>(a.T) * a.k;
-  for (int i = threadIdx.x; i < pairs && first + i < all; i += 256) {
-    const int e = a.experts[first + i];
-    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E)) atomicAdd(&s_held[e], 1);
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += 256) held[static_cast<int64_t>(blockIdx.x) * a.E + e] = s_held[e];
+// A counting sort of the choices by expert.  Runs of tokens are counted (in k_route, or
+// here for a choice made elsewhere); then each run's choices find their rows behind
+// those of the same expert in earlier runs.  A single run is done in one launch.
+__global__ __launch_bounds__(1024) void k_plan_count(PlanArgs a, int run_tokens, uint16_t* held, int pitch) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  int32_t* s_pick = reinterpret_cast<int32_t*>(lds);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * run_tokens, first = t0 * a.k;
+  const int n = static_cast<int>(min(static_cast<int64_t>(run_tokens), a.T - t0)) * a.k;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) s_pick[i] = a.experts[first + i];
+  int32_t* s_count = s_pick + run_tokens * a.k;
+  plan_run(a, gridDim.x == 1, s_pick, n, static_cast<uint32_t>(first), held, pitch, s_count, s_count + a.E, s_count + 2 * a.E + 1);
 }
 
-// held [runs, E] to the sum over earlier runs, total [E]; a thread an expert.
-__global__ __launch_bounds__(64) void k_plan_sum(int32_t* held, int64_t runs, int32_t E, int32_t* total) {
-  const int e = blockIdx.x * 64 + threadIdx.x;
-  if (e >= E) return;
+// Many runs: held [runs, pitch] to sums [runs + 1, pitch] over earlier runs; a wave an expert.
+__global__ __launch_bounds__(256) void k_plan_sum(const uint16_t* held, int64_t runs, int pitch, int32_t* sums) {
+  const int e = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   int32_t sum = 0;
-  for (int64_t r = 0; r < runs; ++r) {
-    const int32_t n = held[r * E + e];
-    held[r * E + e] = sum;
-    sum += n;
+  for (int64_t r0 = 0; r0 < runs; r0 += 64) {
+    const int64_t r = r0 + lane;
+    const int32_t n = r < runs ? held[r * pitch + e] : 0, incl = wave_scan(n);
+    if (r < runs) sums[r * pitch + e] = sum + incl - n;
+    sum += __builtin_amdgcn_readlane(incl, 63);
   }
-  total[e] = sum;
+  if (lane == 0) sums[runs * pitch + e] = sum;
 }
 
-__global__ __launch_bounds__(256) void k_plan_place(PlanArgs a, int pairs, const int32_t* held, const int32_t* total) {
-  extern __shared__ uint32_t s_mask[];                          // [E][words], then the experts' first rows [E + 1]
-  const int words = pairs / 32;
-  int32_t* s_first = reinterpret_cast<int32_t*>(s_mask + a.E * words);
-  for (int i = threadIdx.x; i < a.E * words; i += 256) s_mask[i] = 0;
-  if (threadIdx.x < 64) {                                       // exclusive sums over the experts, by one wave
-    int32_t sum = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64) {
-      const int e = e0 + threadIdx.x;
-      int32_t n = e < a.E ? total[e] : 0, incl = n;
+// Workgroups place `each` runs.  With sums they are taken from there; else a workgroup sums
+// the earlier runs' counts and all of them itself: a thread 8 neighbouring experts of every
+// so many runs, then over the lanes and waves.  (8191 tokens, 256 experts: 256 runs, 128 KB of
+// counts for each of 32 workgroups.)
+// LDS: [pitch] of earlier runs, [pitch] of all, [2][16][pitch] partial sums or [16][E] counts of the
+// waves, and the experts' first rows [E + 1].
+__global__ __launch_bounds__(1024) void k_plan_place(PlanArgs a, int run_tokens, int64_t runs, int each, const uint16_t* held, int pitch,
+                                                     const int32_t* sums) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  int32_t* s_before = reinterpret_cast<int32_t*>(lds);
+  int32_t* s_total = s_before + pitch;
+  int32_t* s_held = s_total + pitch;
+  int32_t* s_first = s_held + (sums ? 16 * a.E : 32 * pitch);
+  const int64_t run0 = static_cast<int64_t>(blockIdx.x) * each, t0 = run0 * run_tokens, first = t0 * a.k;
+  const int n = static_cast<int>(min(static_cast<int64_t>(run_tokens) * each, a.T - t0)) * a.k;
+  const int e0 = threadIdx.x < n ? a.experts[first + threadIdx.x] : -1;
+  if (sums) {
+    for (int e = threadIdx.x; e < pitch; e += 1024) {
+      s_before[e] = sums[run0 * pitch + e];
+      s_total[e] = sums[runs * pitch + e];
+    }
+  } else {
+    const int columns = pitch / 8, shift = __ffs(columns) - 1, strips = 1024 >> shift;     // (a power of two)
+    const int column = threadIdx.x & (columns - 1), strip = threadIdx.x >> shift;
+    int32_t before[8] = {}, total[8] = {};
+    for (int r0 = strip; r0 < static_cast<int>(runs); r0 += 8 * strips) {
+      u32x4_t v[8];                                             // 8 loads on their way at once
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int32_t o = __shfl_up(incl, d, 64);
-        if (static_cast<int>(threadIdx.x) >= d) incl += o;
+      for (int b = 0; b < 8; ++b) {
+        const int r = r0 + b * strips;
+        v[b] = u32x4_t{0, 0, 0, 0};
+        if (r < runs) v[b] = *reinterpret_cast<const u32x4_t*>(held + static_cast<int64_t>(r) * pitch + 8 * column);
       }
-      if (e < a.E) s_first[e] = sum + incl - n;
-      sum += __shfl(incl, 63, 64);
+#pragma unroll
+      for (int b = 0; b < 8; ++b) {
+        const bool earlier = r0 + b * strips < run0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int32_t c = static_cast<int32_t>((v[b][i / 2] >> (16 * (i & 1))) & 0xFFFFu);
+          total[i] += c;
+          before[i] += earlier ? c : 0;
+        }
+      }
     }
-    if (threadIdx.x == 0) s_first[a.E] = sum;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // lanes of a wave with the same column: around the rows of 16, then across them
+    auto turn = [&](auto by) {
+      if (columns > by) return;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        before[i] += lane_move<0x120 + by, 0xF>(before[i]);
+        total[i] += lane_move<0x120 + by, 0xF>(total[i]);
+      }
+    };
+    auto cross = [&](auto by) {
+      if (columns > by) return;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t x, y;
+        both<by>(static_cast<uint32_t>(before[i]), x, y);
+        before[i] = static_cast<int32_t>(x + y);
+        both<by>(static_cast<uint32_t>(total[i]), x, y);
+        total[i] = static_cast<int32_t>(x + y);
+      }
+    };
+    turn(std::integral_constant<int, 1>{});
+    turn(std::integral_constant<int, 2>{});
+    turn(std::integral_constant<int, 4>{});
+    turn(std::integral_constant<int, 8>{});
+    cross(std::integral_constant<int, 16>{});
+    cross(std::integral_constant<int, 32>{});
+    // waves of the same column: every columns / 64-th, or all
+    const int stride = columns > 64 ? columns / 64 : 1, rows = 16 / stride;
+    if (lane < columns) {
+      typedef int i32x4 __attribute__((ext_vector_type(4)));
+      i32x4* part = reinterpret_cast<i32x4*>(s_held + (wave / stride) * pitch + 8 * column);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        part[h] = i32x4{before[4 * h], before[4 * h + 1], before[4 * h + 2], before[4 * h + 3]};
+        part[4 * pitch + h] = i32x4{total[4 * h], total[4 * h + 1], total[4 * h + 2], total[4 * h + 3]};
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 2 * pitch; e += 1024) {       // (s_total follows s_before)
+      const int32_t* part = s_held + (e < pitch ? e : e + 15 * pitch);
+      int32_t sum = 0;
+#pragma unroll 8
+      for (int r = 0; r < rows; ++r) sum += part[r * pitch];
+      s_before[e] = sum;
+    }
   }
   __syncthreads();
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * pairs, all = static_cast<int64_t>(a.T) * a.k;
-  const int n = static_cast<int>(all - first < pairs ? all - first : pairs);
-  for (int i = threadIdx.x; i < n; i += 256) {
-    const int e = a.experts[first + i];
-    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E)) atomicOr(&s_mask[e * words + i / 32], 1u << (i % 32));
-  }
+  if (threadIdx.x < 64) first_rows(s_total, a.E, s_first);
+  __syncthreads();
+  const int32_t end = s_first[a.E];
   if (blockIdx.x == 0)
-    for (int e = threadIdx.x; e <= a.E; e += 256) a.offsets[e] = s_first[e];
+    for (int e = threadIdx.x; e <= a.E; e += 1024) a.offsets[e] = s_first[e];
+  for (int e = threadIdx.x; e < a.E; e += 1024) s_before[e] += s_first[e];
+  for (int i = threadIdx.x; i < n; i += 1024)
+    if (first + i >= end) a.tokens[first + i] = -1;             // a row that belongs to nobody
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += 256) {
-    const int e = a.experts[first + i];
-    int32_t row = -1;
-    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(a.E)) {
-      row = s_first[e] + held[static_cast<int64_t>(blockIdx.x) * a.E + e];
-      for (int w = 0; w < i / 32; ++w) row += __popc(s_mask[e * words + w]);
-      row += __popc(s_mask[e * words + i / 32] & ((1u << (i % 32)) - 1));
-      a.tokens[row] = static_cast<int32_t>((first + i) / a.k);
-    }
-    a.slots[first + i] = row;
-    if (first + i >= s_first[a.E]) a.tokens[first + i] = -1;    // a row that belongs to nobody
-  }
+  place(a, a.experts + first, e0, n, static_cast<uint32_t>(first), s_before, s_held);
 }
 
 // ---- rows --------------------------------------------------------------------------
@@ -556,19 +877,104 @@ dim3 row_grid(const RowsArgs& a, int n) { return dim3(a.T, static_cast<uint32_t>
 
 }  // namespace
 
-hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
+namespace {
+
+// Runs of a plan: the tokens of one workgroup, 4 to 16 waves of them.  One workgroup takes
+// all it can hold, which spares a launch; beyond, the smallest that are no more than the
+// compute units, so that the waves have a vector unit each.
+int lanes_of(int32_t E) { return E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : E <= 64 ? 8 : E <= 128 ? 16 : E <= 256 ? 32 : 64; }
+int per_lane(int32_t E) { return E > 512 ? 16 : 8; }
+struct Runs {
+  int waves, tokens;         // of a workgroup
+  int64_t runs;
+  int pitch;                 // of the counts
+  int64_t each;              // runs of a workgroup of k_plan_place, or 0: the counts are summed first
+  size_t held_bytes, bytes;  // of the counts, and with the sums
+};
+// Every workgroup of k_plan_place reads all counts: fewer workgroups where there are many, so
+// that together they read 16 MB (2 us), and a launch that sums first where those would be too few.
+Runs runs_of(int64_t T, int32_t E, int waves) {
+  const int of_wave = 64 / lanes_of(E), tokens = waves * of_wave;
+  const int64_t needed = (T + of_wave - 1) / of_wave, runs = T > 0 ? (T + tokens - 1) / tokens : 1;
+  if (needed < waves) waves = needed > 0 ? static_cast<int>(needed) : 1;
+  const int pitch = lanes_of(E) * per_lane(E);
+  int64_t each = (runs * runs * pitch * 2 + (int64_t{16} << 20) - 1) >> 24;
+  if (each > 8) each = 0;
+  const size_t held = static_cast<size_t>(runs) * pitch * 2, sums = each == 0 ? static_cast<size_t>(runs + 1) * pitch * 4 : 0;
+  return {waves, tokens, runs, pitch, each, held, held + sums};
+}
+int waves_for(int64_t T, int32_t E, int most) {
+  const int64_t needed = (T + 64 / lanes_of(E) - 1) / (64 / lanes_of(E));
+  if (needed <= most) return most;
+  int waves = most < 4 ? most : 4;
+  while (waves < most && needed > static_cast<int64_t>(waves) * device_cu_count()) waves *= 2;
+  return waves;
+}
+// Waves of a run of a choice with k a token: its choices fit 32 KB of LDS (k_route's always do: k <= E).
+int run_waves(int32_t E, int32_t k) {
+  int waves = 16;
+  while (waves > 1 && waves * (64 / lanes_of(E)) * k * 4 > 32768) waves /= 2;
+  return waves;
+}
+
+size_t plan_lds(int32_t E, int waves) { return static_cast<size_t>(2 * E + 1 + waves * E) * 4; }
+
+template <typename K>
+void allow_lds(K kernel) {
+  (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+  (void)hipGetLastError();
+}
+
+// The second half, behind the counts.
+hipError_t launch_place(const PlanArgs& a, const Runs& r, uint16_t* held, hipStream_t stream) {
+  static const bool done = [] {
+    allow_lds(k_plan_place);
+    return true;
+  }();
+  (void)done;
+  int32_t* sums = nullptr;
+  if (r.each == 0) {
+    sums = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(held) + r.held_bytes);
+    k_plan_sum<<<r.pitch / 4, 256, 0, stream>>>(held, r.runs, r.pitch, sums);
+  }
+  const int64_t each = r.each == 0 ? 1 : r.each;
+  const size_t behind = static_cast<size_t>(r.each == 0 ? 16 * a.E : 32 * r.pitch), lds = (2 * r.pitch + a.E + 1 + behind) * 4;
+  k_plan_place<<<static_cast<uint32_t>((r.runs + each - 1) / each), 1024, lds, stream>>>(a, r.tokens, r.runs, static_cast<int>(each), held,
+                                                                                        r.pitch, sums);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteArgs& args, const PlanArgs& plan, void* ws, hipStream_t stream) {
+  RouteArgs a = args;
   const bool wide = a.bias || (a.groups > 1 && a.top2);
-  return with_lanes(a.E, [&](auto per, auto lanes) {
-    constexpr int PER = per, L = lanes, kWaves = PER == 16 ? 2 : 4, kTokens = kWaves * (64 / L);
-    const size_t bytes = kWaves * 64 * PER * (a.groups > 1 ? 24 : 8);
-    const int grid = (a.T + kTokens - 1) / kTokens;
+  const int size = a.E / a.groups, per = per_lane(a.E), lanes = size / per;
+  a.lanes = a.groups > 1 && size % per == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  const bool through_lds = a.groups > 1 && a.lanes == 0;
+  const Runs r = runs_of(a.T, a.E, waves_for(a.T, a.E, through_lds ? 4 : 16));
+  size_t bytes = (static_cast<size_t>(r.tokens) * a.k * 4 + 15) / 16 * 16;
+  a.group_lds = static_cast<int32_t>(bytes);
+  if (through_lds) bytes += static_cast<size_t>(r.waves) * 64 * per * 16;
+  a.plan_lds = static_cast<int32_t>(bytes);
+  if (plan.offsets) bytes += plan_lds(a.E, r.waves);
+  uint16_t* held = static_cast<uint16_t*>(ws);
+  const hipError_t e = with_lanes(a.E, [&](auto per_c, auto lanes_c) {
+    constexpr int PER = per_c, L = lanes_c;
     auto go = [&](auto kernel) {
-      kernel<<<grid, 64 * kWaves, bytes, stream>>>(a);
+      static const bool done = [&] {
+        allow_lds(kernel);
+        return true;
+      }();
+      (void)done;
+      kernel<<<static_cast<uint32_t>(r.runs), 64 * r.waves, bytes, stream>>>(a, plan, held, r.pitch);
       return hipGetLastError();
     };
     if (a.bf16) return wide ? go(k_route<uint16_t, PER, L, true>) : go(k_route<uint16_t, PER, L, false>);
     return wide ? go(k_route<float, PER, L, true>) : go(k_route<float, PER, L, false>);
   });
+  if (e != hipSuccess || !plan.offsets || r.runs == 1) return e;
+  return launch_place(plan, r, held, stream);
 }
 
 hipError_t launch_route_bwd(const RouteArgs& a, const float* grad_weights, void* grad_logits, hipStream_t stream) {
@@ -581,18 +987,26 @@ hipError_t launch_route_bwd(const RouteArgs& a, const float* grad_weights, void*
   });
 }
 
-size_t plan_ws_bytes(int64_t T, int32_t k, int32_t E) { return static_cast<size_t>(plan_runs(T * k, E) + 1) * E * 4; }
+// k_route's shortest runs need the most.
+size_t plan_ws_bytes(int64_t T, int32_t k, int32_t E) {
+  const int waves = run_waves(E, k);
+  const Runs r = runs_of(T, E, waves < 4 ? waves : 4);
+  return r.runs == 1 ? 0 : r.bytes;
+}
 
 hipError_t launch_plan(const PlanArgs& a, void* ws, hipStream_t stream) {
-  const int64_t runs = plan_runs(static_cast<int64_t>(a.T) * a.k, a.E);
-  const int pairs = plan_pairs(a.E);
-  int32_t *total = static_cast<int32_t*>(ws), *held = total + a.E;
-  const uint32_t grid = static_cast<uint32_t>(runs);
-  if (runs > 0) k_plan_count<<<grid, 256, a.E * 4, stream>>>(a, pairs, held);
-  k_plan_sum<<<(a.E + 63) / 64, 64, 0, stream>>>(held, runs, a.E, total);
-  // without a choice one workgroup writes the offsets
-  k_plan_place<<<grid > 0 ? grid : 1, 256, a.E * (pairs / 8) + (a.E + 1) * 4, stream>>>(a, pairs, held, total);
-  return hipGetLastError();
+  const Runs r = runs_of(a.T, a.E, waves_for(a.T, a.E, run_waves(a.E, a.k)));
+  uint16_t* held = static_cast<uint16_t*>(ws);
+  const size_t lds = static_cast<size_t>(r.tokens) * a.k * 4 + plan_lds(a.E, r.runs == 1 ? 16 : 0);
+  static const bool done = [] {
+    allow_lds(k_plan_count);
+    return true;
+  }();
+  (void)done;
+  k_plan_count<<<static_cast<uint32_t>(r.runs), 1024, lds, stream>>>(a, r.tokens, held, r.pitch);
+  if (r.runs == 1) return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess ? e : launch_place(a, r, held, stream);
 }
 
 hipError_t launch_gather(const RowsArgs& a, const void* x, int64_t stride, void* rows, hipStream_t stream) {

@@ -18,6 +18,7 @@ struct RouteArgs {
   float scale;
   float* weights;
   int32_t* experts;
+  int32_t lanes = 0, group_lds = 0, plan_lds = 0;               // of the launch
 };
 
 struct PlanArgs {
@@ -36,7 +37,7 @@ struct RowsArgs {
 };
 
 size_t plan_ws_bytes(int64_t T, int32_t k, int32_t E);
-hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
+hipError_t launch_route(const RouteArgs& a, const PlanArgs& plan, void* ws, hipStream_t stream);   // plan.offsets NULL: no plan
 hipError_t launch_route_bwd(const RouteArgs& a, const float* grad_weights, void* grad_logits, hipStream_t stream);
 hipError_t launch_plan(const PlanArgs& a, void* ws, hipStream_t stream);
 hipError_t launch_gather(const RowsArgs& a, const void* x, int64_t stride, void* rows, hipStream_t stream);

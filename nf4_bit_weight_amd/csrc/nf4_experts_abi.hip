@@ -120,17 +120,13 @@ int nf4_route_fwd(const void* logits, int dtype, int64_t stride, int64_t T, int3
     if (st) return st;
   }
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = hipSuccess;
-  if (T > 0) {
-    const RouteArgs a{logits, dtype == NF4_DTYPE_BF16, stride, static_cast<int32_t>(T), E, k, bias, score == NF4_SCORE_SIGMOID,
-                      group_score == NF4_GROUP_TOP2, renormalize != 0, groups, top_groups, scale, weights, experts};
-    e = launch_route(a, s);
-    if (e == hipSuccess) count_path(NF4_PATH_ROUTE_FWD);
-  }
-  if (e == hipSuccess && plan) {
-    e = launch_plan({experts, static_cast<int32_t>(T), k, E, offsets, tokens, slots}, ws, s);
-    if (e == hipSuccess) count_path(NF4_PATH_EXPERT_PLAN);
-  }
+  const PlanArgs pl{experts, static_cast<int32_t>(T), k, E, offsets, tokens, slots};
+  if (T == 0) return plan ? to_status(launch_plan(pl, ws, s)) : NF4_OK;
+  const RouteArgs a{logits, dtype == NF4_DTYPE_BF16, stride, static_cast<int32_t>(T), E, k, bias, score == NF4_SCORE_SIGMOID,
+                    group_score == NF4_GROUP_TOP2, renormalize != 0, groups, top_groups, scale, weights, experts};
+  const hipError_t e = launch_route(a, pl, ws, s);
+  if (e == hipSuccess) count_path(NF4_PATH_ROUTE_FWD);
+  if (e == hipSuccess && plan) count_path(NF4_PATH_EXPERT_PLAN);
   return to_status(e);
 }
 

@@ -60,10 +60,11 @@ def test_route_refuses(lib):
         assert f(scale=s) == SHAPE
     assert f(E=1025) == f(E=512, k=65, g=1, tg=1) == f(T=1 << 30) == f(T=1 << 26, k=1) == f(score=2) == f(gs=2) == NO
     assert f(dt=2) == DTYPE
-    assert f(l=A + 2) == f(bias=A + 2) == f(w=A + 1) == f(slot=A + 2) == f(ws=BAD) == ALIGN
-    need = lib.nf4_expert_plan_workspace(4, 2, 16)
+    assert f(l=A + 2) == f(bias=A + 2) == f(w=A + 1) == f(slot=A + 2) == f(T=4000, ws=BAD) == ALIGN
+    assert lib.nf4_expert_plan_workspace(4, 2, 16) == 0                     # one workgroup does it all
+    need = lib.nf4_expert_plan_workspace(4000, 2, 16)
     assert 0 < need < BIG
-    assert f(ws=None) == f(wsb=need - 1) == WS
+    assert f(T=4000, ws=None) == f(T=4000, wsb=need - 1) == WS
     assert lib.nf4_expert_plan_workspace(-1, 2, 16) == lib.nf4_expert_plan_workspace(4, 0, 16) == lib.nf4_expert_plan_workspace(4, 2, 0) == BIG
     # without a plan, and without tokens
     assert f(T=0, l=None, w=None, e=None, off=None, tok=None, slot=None, ws=None, wsb=0) == OK
@@ -90,8 +91,8 @@ def test_plan_refuses(lib):
     assert f(e=None) == f(off=None) == f(tok=None) == f(slot=None) == NULL
     assert f(T=-1) == f(k=0) == f(E=0) == SHAPE
     assert f(k=65) == f(E=1025) == f(T=1 << 30) == NO
-    assert f(e=A + 2) == f(ws=BAD) == ALIGN
-    assert f(ws=None) == f(wsb=16) == WS
+    assert f(e=A + 2) == f(T=4000, ws=BAD) == ALIGN
+    assert f(T=4000, ws=None) == f(T=4000, wsb=16) == WS
 
 
 def test_rows_refuse(lib):
