@@ -96,6 +96,14 @@ struct Routed {
   Tensor weights, experts, offsets, tokens, slots;
   int status = 0;
 };
+// Numbers `at` .. of `all` as a tensor of their own.  (The four results of integers share one
+// allocation: at a batch of new tokens allocating takes as long as the kernel.)
+Tensor part_of(const Tensor& all, int64_t at, at::IntArrayRef shape) {
+  auto impl = c10::make_intrusive<at::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+  impl->set_storage_offset(at);
+  impl->set_sizes_contiguous(shape);
+  return Tensor(std::move(impl));
+}
 Routed run_route(const Tensor& logits, const Tensor& bias, const Route& r) {
   const Matrix l = matrix(logits, "logits");
   const int32_t E = small(l.n, "the number of experts");
@@ -105,8 +113,10 @@ Routed run_route(const Tensor& logits, const Tensor& bias, const Route& r) {
   if (bias.defined()) need(bias, "bias", at::kFloat, E, &l.dev);
   const size_t bytes = nf4_expert_plan_workspace(l.rows, r.k, E);
   if (bytes == SIZE_MAX) return {{}, {}, {}, {}, {}, NF4_ERR_UNSUPPORTED};
-  Routed o{fresh({l.rows, r.k}, at::kFloat, l.dev), fresh({l.rows, r.k}, at::kInt, l.dev), fresh({E + 1}, at::kInt, l.dev),
-           fresh({l.rows * r.k}, at::kInt, l.dev), fresh({l.rows, r.k}, at::kInt, l.dev)};
+  const int64_t n = l.rows * r.k;
+  const Tensor all = fresh({3 * n + E + 1}, at::kInt, l.dev);
+  Routed o{fresh({l.rows, r.k}, at::kFloat, l.dev), part_of(all, 0, {l.rows, r.k}), part_of(all, 3 * n, {E + 1}), part_of(all, n, {n}),
+           part_of(all, 2 * n, {l.rows, r.k})};
   const On on(l.dev);
   const Tensor ws = new_workspace(bytes, l.dev);
   o.status = nf4_route_fwd(l.p, l.dtype, l.stride, l.rows, E, r.k, bias.defined() ? bias.data_ptr<float>() : nullptr, r.sigmoid,
@@ -136,6 +146,7 @@ struct RouteNode : torch::autograd::Function<RouteNode> {
     const Routed o = run_route(l, bias ? *bias : Tensor(), r);
     ok(o.status, "nf4_route_fwd");
     ctx->mark_non_differentiable({o.experts, o.offsets, o.tokens, o.slots});
+    ctx->set_materialize_grads(false);                         // no zeros for the integers
     ctx->save_for_backward({l, o.weights, o.experts});
     ctx->saved_data["sigmoid"] = r.sigmoid;
     ctx->saved_data["renorm"] = r.renorm;
@@ -145,6 +156,7 @@ struct RouteNode : torch::autograd::Function<RouteNode> {
   }
   static variable_list backward(AutogradContext* ctx, variable_list grad) {
     once_only("nf4_route", grad[0]);
+    if (!grad[0].defined()) return {Tensor(), Tensor(), Tensor()};
     const auto s = ctx->get_saved_variables();
     Route r;
     r.sigmoid = ctx->saved_data["sigmoid"].toBool();
