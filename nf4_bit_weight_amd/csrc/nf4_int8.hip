@@ -171,31 +171,25 @@ struct RowTile {
 template <int BM>
 __device__ __forceinline__ RowTile row_tile(const Int8Args& a, int mt) {
   if (!a.offsets) return {static_cast<int64_t>(mt) * BM, a.M, 0};
-  const int lane = static_cast<int>(threadIdx.x & 63);
+  const int lane = static_cast<int>(threadIdx.x & 63), M = static_cast<int>(a.M);
   int before = 0;
   for (int e0 = 0; e0 <= a.E; e0 += 64) {
     const int e = e0 + lane;
-    int64_t lo = 0, hi = 0;
+    int lo = 0, hi = 0;
     if (e <= a.E) {
       lo = a.offsets[e];
-      hi = e < a.E ? a.offsets[e + 1] : a.M;
-      lo = lo < 0 ? 0 : (lo > a.M ? a.M : lo);
-      hi = hi < lo ? lo : (hi > a.M ? a.M : hi);
+      hi = e < a.E ? a.offsets[e + 1] : M;
+      lo = min(max(lo, 0), M);
+      hi = min(max(hi, lo), M);
     }
-    const int tiles = static_cast<int>((hi - lo + BM - 1) / BM);
-    int incl = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += o;
-    }
-    const int at = before + incl - tiles;
+    const int tiles = (hi - lo + BM - 1) / BM, incl = wave_scan(tiles), at = before + incl - tiles;
     const unsigned long long hit = __ballot(mt >= at && mt < before + incl);
     if (hit) {
-      const int l = __ffsll(static_cast<long long>(hit)) - 1;
-      return {__shfl(lo, l, 64) + static_cast<int64_t>(mt - __shfl(at, l, 64)) * BM, __shfl(hi, l, 64), e0 + l};
+      const int l = uniform(__ffsll(static_cast<long long>(hit)) - 1);
+      return {__builtin_amdgcn_readlane(lo, l) + static_cast<int64_t>(mt - __builtin_amdgcn_readlane(at, l)) * BM,
+              __builtin_amdgcn_readlane(hi, l), e0 + l};
     }
-    before += __shfl(incl, 63, 64);
+    before += __builtin_amdgcn_readlane(incl, 63);
   }
   return {0, 0, 0};
 }
@@ -679,7 +673,7 @@ struct TileShape {
   int bm, bn, cost;
 };
 constexpr TileShape kShapes[] = {{64, 64, 13}, {128, 64, 20}, {128, 128, 33}, {256, 128, 63}, {256, 256, 96}};
-constexpr TileShape kGroupedShapes[] = {{64, 64, 13}, {0, 0, 0}, {128, 128, 30}, {0, 0, 0}, {256, 256, 96}};
+constexpr TileShape kGroupedShapes[] = {{64, 64, 17}, {0, 0, 0}, {128, 128, 40}, {0, 0, 0}, {256, 256, 97}};
 
 int best_shape(const Int8Args& a, int cus) {
   int best = 0;
