@@ -72,7 +72,7 @@ SHAPES = [(1, 1, 1), (1, 16, 64), (1, 4096, 4096), (2, 100, 300), (3, 33, 128), 
           (512, 4096, 128), (1000, 4100, 500), (1024, 4096, 640), (520, 4000, 1000), (2048, 4096, 128), (2048, 4000, 300),
           (4096, 4096, 256), (2500, 3500, 700),
           # few rows: channels 16, 32 and 64 a workgroup, K in one to eight parts and beyond what is in flight
-          (5, 14336, 128), (16, 7300, 384), (1, 15000, 600), (20, 4096, 1300), (33, 8100, 2200), (50, 1000, 8000), (64, 4096, 200), (2, 40, 20000)]
+          (5, 14336, 1100), (3, 14336, 128), (16, 7300, 384), (1, 15000, 600), (20, 4096, 1300), (33, 8100, 2200), (50, 1000, 8000), (64, 4096, 200), (2, 40, 20000)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
