@@ -8,14 +8,16 @@
  * Conventions (memory, streams, errors, status codes) are those of nf4.h: all
  * pointers are device memory of the caller, work is enqueued asynchronously
  * on `stream`, nothing is allocated, freed or retained, an error enqueues
- * nothing.  Sums run in a fixed order (the only atomics are bits of integer
- * masks), so repeated calls on the same inputs give bitwise identical outputs.
+ * nothing.  Sums run in a fixed order (the only atomics count integers),
+ * so repeated calls on the same inputs give bitwise identical outputs.
  * Every call can be captured into a HIP graph.  Written tensors are contiguous
  * and overlap nothing that the call reads.
  *
  * Sizes.  T tokens, E experts (1 to 1024), k choices per token (1 to 64, at
- * most E).  T * k is at most 2^30, and a launch holds fewer than 2^32 threads
- * (else NF4_ERR_UNSUPPORTED).  dtype is NF4_DTYPE_F32 or NF4_DTYPE_BF16.
+ * most E; of a choice made elsewhere, which may name an expert twice, also more).
+ * T * k is at most 2^30, a row has at most 2^23 elements, and a launch holds fewer
+ * than 2^32 threads (else NF4_ERR_UNSUPPORTED).  dtype is NF4_DTYPE_F32 or
+ * NF4_DTYPE_BF16.
  *
  * The plan of a choice `experts` int32 [T, k]:
  *   offsets  int32 [E + 1]  rows offsets[e] .. offsets[e+1]-1 are expert e's, as
@@ -72,8 +74,8 @@ int nf4_route_fwd(const void* logits, int dtype, int64_t stride, int64_t T, int3
 
 /*
  * nf4_route_bwd -- grad_logits [T, E] in dtype from grad_weights f32 [T, k] and
- * the forward call's logits, weights and experts.  The choice itself has no
- * gradient; grad_weights in places without an expert is not read into it.
+ * the forward call's logits, weights and experts (none twice for a token).  The
+ * choice itself has no gradient; grad_weights in places without an expert is not read into it.
  */
 int nf4_route_bwd(const float* grad_weights, const void* logits, int dtype,
                   int64_t stride, int64_t T, int32_t E, int32_t k, const float* weights,

@@ -28,8 +28,8 @@ int check_choices(int64_t T, int32_t E, int32_t k) {
 int check_rows(int dtype, int64_t T, int64_t H, int32_t k) {
   if (!is_float(dtype)) return NF4_ERR_DTYPE;
   if (T < 0 || H < 0 || k < 1) return NF4_ERR_SHAPE;
-  if (k > 64 || T > (1 << 30) / k || H > 1 << 24) return NF4_ERR_UNSUPPORTED;
-  return launchable(T * ((H + 255) / 256), 256) ? NF4_OK : NF4_ERR_UNSUPPORTED;
+  if (k > 64 || T > (1 << 30) / k || H > 1 << 23) return NF4_ERR_UNSUPPORTED;   // (a grid has 65535 workgroups across)
+  return launchable(T * (H > 256 ? (H + 255) / 256 : 1), 256) ? NF4_OK : NF4_ERR_UNSUPPORTED;
 }
 
 int check_plan(const int32_t* experts, int64_t T, const int32_t* offsets, const int32_t* tokens, const int32_t* slots, const void* ws,

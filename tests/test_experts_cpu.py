@@ -122,6 +122,13 @@ def test_rows_refuse(lib):
     assert combine(T=0, rows=None, w=None, slots=None, out=None) == gather_bwd(T=0, g=None, slots=None, out=None) == OK
 
 
+def test_rows_refuse_what_no_launch_holds(lib):
+    """A launch has at most 65535 workgroups across a row and 2^32 threads, also of rows without elements."""
+    assert lib.nf4_expert_gather(A, 0, 64, 4, (1 << 23) + 1, 2, A, A, A, 1, None) == NO
+    assert lib.nf4_expert_combine_fwd(A, 0, 4, 65536 * 256, 2, A, A, A, None) == NO
+    assert lib.nf4_expert_combine_bwd(None, 0, None, 0, 1 << 24, 0, 1, A, A, A, A, A, 1, None) == NO
+
+
 def test_int8_refuses(lib):
     base = dict(x=A, dt=1, st=256, xs=None, M=4, q=A, s=A, N=32, K=256, bias=None, y=A, yd=0, ws=A, wsb=1 << 30)
 
