@@ -208,7 +208,9 @@ int nf4_matmul_bwd_input(const void* grad_y, int64_t M,
  *   W-args   the expert stack [E, N, K] quantised as ONE tensor of E*N rows;
  *            N, K are per-expert.  Requires K % 64 == 0.
  *   y        bf16 [total_M, N]
- * Routing, gather and scatter stay with the caller.
+ * offsets[E] may lie before total_M (choices that name no expert): the rows
+ * behind it are left as they were, here and in the other grouped calls.
+ * Routing, gather and combine are calls of their own (nf4_experts.h).
  */
 int nf4_grouped_matmul_fwd(const void* x, const int32_t* offsets, int32_t E,
                            int64_t total_M,

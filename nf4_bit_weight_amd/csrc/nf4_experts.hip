@@ -296,7 +296,11 @@ __device__ __forceinline__ void plan_run(const PlanArgs& a, bool only, const int
 // in 64 bits, since 8191 x 256 scores hold several pairs that fp32 rounding would turn round.
 //
 // A workgroup's tokens are a run of the plan: it counts their choices for k_plan_place, or,
-// as the only one, places them itself (one launch for a batch of new tokens).
+// as the only one, places them itself (one launch for a batch of new tokens: 4.8 us for one).
+//
+// What bounds it: instructions.  8191 tokens, 256 experts, sigmoid with a bias in 8 groups: 15.5 us, 1630
+// vector instructions a wave of two tokens, most of them the 64-bit scores and keys; the bytes take 1.9 us.
+// 16384 tokens, 64 experts, bf16 and softmax: 6.4.
 template <typename T, int PER, int L, bool WIDE>
 __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint16_t* held, int pitch) {
   constexpr int kTokens = 64 / L, kOf = L * PER;
@@ -535,7 +539,7 @@ __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint
 //   softmax, renormalised   [i chosen] w_i (g_i - D / scale)
 //   sigmoid                 [i chosen] g_i w_i (1 - s_i)
 //   sigmoid, renormalised   [i chosen] w_i (1 - s_i) (g_i - D / scale)
-// Lanes as in k_route; the token's row is put together in LDS.
+// Lanes as in k_route; the token's row is put together in LDS.  (16384 tokens, 64 experts, bf16: 3.8 us.)
 template <typename T, int PER, int L>
 __global__ __launch_bounds__(PER == 16 ? 128 : 256) void k_route_bwd(RouteArgs a, const float* grad, T* out) {
   constexpr int kWaves = PER == 16 ? 2 : 4, kTokens = 64 / L, kOf = L * PER;
@@ -642,7 +646,7 @@ __global__ __launch_bounds__(256) void k_plan_sum(const uint16_t* held, int64_t 
 // Workgroups place `each` runs.  With sums they are taken from there; else a workgroup sums
 // the earlier runs' counts and all of them itself: a thread 8 neighbouring experts of every
 // so many runs, then over the lanes and waves.  (8191 tokens, 256 experts: 256 runs, 128 KB of
-// counts for each of 32 workgroups.)
+// counts for each of 128 workgroups, 7.9 us, a chain of short steps.)
 // LDS: [pitch] of earlier runs, [pitch] of all, [2][16][pitch] partial sums or [16][E] counts of the
 // waves, and the experts' first rows [E + 1].
 __global__ __launch_bounds__(1024) void k_plan_place(PlanArgs a, int run_tokens, int64_t runs, int each, const uint16_t* held, int pitch,
@@ -786,7 +790,8 @@ __device__ __forceinline__ float lane_value(float x, int lane) {
 }
 constexpr int kAtOnce = 2;   // rows of a token on their way together (8: 33 us for 29 at 4096 x 8 of 2048, 4 the same)
 
-// Workgroups: one a token and 256 vectors of its row.
+// Workgroups: one a token and 256 vectors of its row, which is read once and written k times.
+// What bounds it are the bytes: 4096 tokens x 8 of 2048 in bf16 25.5 us, 5.9 TB/s into the last-level cache.
 template <typename T, int N>
 __global__ __launch_bounds__(256) void k_gather(RowsArgs a, const T* x, int64_t stride, T* rows) {
   const int64_t t = blockIdx.x, h = (static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x) * N;
@@ -804,7 +809,8 @@ __global__ __launch_bounds__(256) void k_gather(RowsArgs a, const T* x, int64_t 
   for (int64_t r = t * a.k > end ? t * a.k : end; r < (t + 1) * a.k; ++r) v.put(rows + r * a.H + h);
 }
 
-// out[t] = sum_j w_j rows[slot_j] (weights NULL: ones)
+// out[t] = sum_j w_j rows[slot_j] (weights NULL: ones).  Bound by the bytes: 4095 tokens x 8 of 2048
+// in bf16 22 us where the last-level cache holds the rows, 40 from memory.
 template <typename T, int N>
 __global__ __launch_bounds__(256) void k_combine(RowsArgs a, const T* rows, const float* weights, T* out) {
   const int64_t t = blockIdx.x, h = (static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x) * N;
@@ -832,7 +838,8 @@ __global__ __launch_bounds__(256) void k_combine(RowsArgs a, const T* rows, cons
   if (h < a.H) sum.put(out + t * a.H + h);
 }
 
-// A workgroup a token, kAtOnce of its choices at a time.
+// A workgroup a token, kAtOnce of its choices at a time: grad_out is read k / kAtOnce times, from
+// the L2.  (4095 x 8 of 2048 in bf16, 285 MB: 48 us, 5.9 TB/s.)
 template <typename T, int N>
 __global__ __launch_bounds__(256) void k_combine_bwd(RowsArgs a, const T* grad, int64_t stride, const T* rows, const float* weights,
                                                      T* grad_rows, float* grad_weights) {
@@ -925,7 +932,8 @@ struct Runs {
   size_t held_bytes, bytes;  // of the counts, and with the sums
 };
 // Every workgroup of k_plan_place reads all counts: fewer workgroups where there are many, so
-// that together they read 16 MB (2 us), and a launch that sums first where those would be too few.
+// that together they read 16 MB (from the L2s mostly), and a launch that sums first where those
+// would be too few.
 Runs runs_of(int64_t T, int32_t E, int waves) {
   const int of_wave = 64 / lanes_of(E), tokens = waves * of_wave;
   const int64_t needed = (T + of_wave - 1) / of_wave, runs = T > 0 ? (T + tokens - 1) / tokens : 1;

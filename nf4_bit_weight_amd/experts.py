@@ -24,6 +24,9 @@ before the capture.
     rows = nf4_expert_gather(x, r)                              # [T * 8, H], sorted by expert
     h = nf4_grouped_linear(rows, r.offsets, w_up, E)            # or nf4_int8_grouped_matmul
     y = nf4_expert_combine(nf4_grouped_linear(act(h), r.offsets, w_down, E), r)
+
+The grouped calls in 4 and 8 bits write no row behind offsets[E]; none of the calls here
+reads one.
 """
 
 from __future__ import annotations

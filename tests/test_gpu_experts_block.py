@@ -105,6 +105,21 @@ def test_padding_tokens_pass_through_the_layer():
     assert bool((y[T - 7:] == 0).all()) and bool((g[T - 7:] == 0).all())
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("tokens,some", [(6, 3), (50, 43), (700, 300)])
+def test_grouped_calls_leave_the_rows_of_nobody(bits, tokens, some):
+    code = torch.from_numpy(WL.nf4_code_np() if bits == 4 else WL.int8_code_np()).to(DEV)
+    w = nf4_quantize(WL.gpu_weight_f32(E * MID, HID, seed=510, device=DEV, std=0.08), code, bits=bits).per_expert(E)
+    logits = R.normal(11, tokens, E).to(DEV)
+    logits[some:] = -float("inf")
+    r = nf4_route(logits, K)
+    for f, n, m in ((nf4_grouped_matmul_fwd, HID, MID), (nf4_grouped_matmul_bwd_input, MID, HID)):
+        rows = R.normal(12, tokens * K, n).to(torch.bfloat16).to(DEV)
+        out = torch.full((tokens * K, m), 7.0, dtype=torch.bfloat16, device=DEV)
+        f(rows, r.offsets, w, E, out)
+        assert bool((out[some * K:] == 7).all()) and bool((out[: some * K] != 7).any(1).all())
+
+
 def served(x, logits, w8):
     r = nf4_route(logits, K, **HOW)
     xq = nf4_int8_quantize(x)                                    # once for both projections
