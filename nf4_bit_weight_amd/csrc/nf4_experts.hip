@@ -41,9 +41,9 @@ __device__ __forceinline__ float number32(uint32_t r) {       // and back
   return __builtin_bit_cast(float, r & 0x80000000u ? r & 0x7FFFFFFFu : ~r);
 }
 __device__ __forceinline__ uint64_t rank64(double x) {
-  if (x != x) return ~uint64_t{0};
   const uint64_t u = x == 0.0 ? 0u : __builtin_bit_cast(uint64_t, x);
-  return u >> 63 ? ~u : u | uint64_t{1} << 63;
+  const uint64_t flip = static_cast<uint64_t>(static_cast<int64_t>(u) >> 63) | uint64_t{1} << 63;
+  return x != x ? ~uint64_t{0} : u ^ flip;
 }
 
 // This lane's value and the one of the lane M further in a butterfly over equal
@@ -98,6 +98,21 @@ __device__ __forceinline__ V across(V v, F f) {
   } else {
     return v;
   }
+}
+
+// The largest of the L lanes' values: of the high halves, then of the low halves beside that one.  (Two
+// searches of 32 bits, whose maxima take the lane moves with them, are 24 instructions for the 40 of one of 64.)
+template <int L>
+__device__ __forceinline__ uint64_t largest(uint64_t v) {
+  auto most = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
+  const uint32_t high = static_cast<uint32_t>(v >> 32), top = across<L>(high, most);
+  return static_cast<uint64_t>(top) << 32 | across<L>(high == top ? static_cast<uint32_t>(v) : 0u, most);
+}
+// The lanes of a token's L that stand below `lane`, as a ballot has them.
+template <int L>
+__device__ __forceinline__ uint64_t lanes_below(int lane) {
+  const uint64_t token = ~uint64_t{0} << (lane & ~(L - 1));
+  return ((uint64_t{1} << lane) - 1) & token;
 }
 
 // An expert in the running.  Where 32 bits order the scores, their rank and the
@@ -174,15 +189,15 @@ __device__ __forceinline__ double reciprocal64(double x) {
 __device__ __forceinline__ float exp_from(float l, float top) { return l == -INFINITY ? 0.0f : expf(l - top); }
 
 // This lane's choice (-1: none), the lanes of its wave with the same expert below it, and
-// the wave's counts in s_held [waves][E]: the lanes of an expert are found by one ballot for each
+// the counts of its wave in s_held [waves][E] (waves: those with choices): the lanes of an expert are found by one ballot for each
 // bit of its number.  No count depends on who comes first.
 struct Claim {
   int expert;
   int below;
   bool some;
 };
-__device__ __forceinline__ Claim claim(int e, int32_t E, int32_t* s_held) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+__device__ __forceinline__ Claim claim(int e, int32_t E, int waves, int32_t* s_held) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   for (int x = threadIdx.x; x < waves * E; x += blockDim.x) s_held[x] = 0;
   const bool some = static_cast<uint32_t>(e) < static_cast<uint32_t>(E);
   uint64_t same = __ballot(some);
@@ -197,8 +212,7 @@ __device__ __forceinline__ Claim claim(int e, int32_t E, int32_t* s_held) {
   return {e, below, some};
 }
 // s_held to the sums over earlier waves behind `at`; all of it comes back.
-__device__ __forceinline__ int32_t sum_waves(int32_t* s_held, int32_t E, int e, int32_t at) {
-  const int waves = blockDim.x >> 6;
+__device__ __forceinline__ int32_t sum_waves(int32_t* s_held, int32_t E, int waves, int e, int32_t at) {
   for (int w0 = 0; w0 < waves; w0 += 8) {
     int32_t n[8];
 #pragma unroll
@@ -219,12 +233,12 @@ __device__ __forceinline__ void settle(const PlanArgs& a, const Claim& c, int32_
 // Rows of the choices [0, n) of `choices` (in LDS or memory) behind s_base, by expert
 // and then in order, a workgroup's threads of them at a time; e is this thread's first one.
 __device__ __forceinline__ void place(const PlanArgs& a, const int32_t* choices, int e, int n, uint32_t first, int32_t* s_base, int32_t* s_held) {
-  const int wave = threadIdx.x >> 6, threads = blockDim.x;
+  const int wave = threadIdx.x >> 6, threads = blockDim.x, waves = (min(n, threads) + 63) / 64;
   for (int c = 0; c < n; c += threads) {
     const int i = c + threadIdx.x;
     if (c > 0) e = i < n ? choices[i] : -1;
-    const Claim mine = claim(e, a.E, s_held);
-    for (int x = threadIdx.x; x < a.E; x += threads) s_base[x] = sum_waves(s_held, a.E, x, s_base[x]);
+    const Claim mine = claim(e, a.E, waves, s_held);
+    for (int x = threadIdx.x; x < a.E; x += threads) s_base[x] = sum_waves(s_held, a.E, waves, x, s_base[x]);
     __syncthreads();
     if (i < n) settle(a, mine, mine.some ? s_held[wave * a.E + mine.expert] + mine.below : -1, first + i);
     if (c + threads < n) __syncthreads();
@@ -235,11 +249,17 @@ __device__ __forceinline__ void place(const PlanArgs& a, const int32_t* choices,
 __device__ __forceinline__ void first_rows(const int32_t* s_count, int32_t E, int32_t* s_first) {
   const int lane = threadIdx.x;
   int32_t sum = 0;
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const int e = e0 + lane;
-    const int32_t n = e < E ? s_count[e] : 0, incl = wave_scan(n);
-    if (e < E) s_first[e] = sum + incl - n;
-    sum += __builtin_amdgcn_readlane(incl, 63);
+  for (int e0 = 0; e0 < E; e0 += 256) {
+    int32_t n[4], incl[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n[i] = e0 + 64 * i + lane < E ? s_count[e0 + 64 * i + lane] : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) incl[i] = wave_scan(n[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (e0 + 64 * i + lane < E) s_first[e0 + 64 * i + lane] = sum + incl[i] - n[i];
+      sum += __builtin_amdgcn_readlane(incl[i], 63);
+    }
   }
   if (lane == 0) s_first[E] = sum;
 }
@@ -262,8 +282,9 @@ __device__ __forceinline__ void plan_run(const PlanArgs& a, bool only, const int
   const bool once = only && n <= threads;                      // a choice a thread: counted and placed in one pass
   Claim mine{};
   if (once) {
-    mine = claim(threadIdx.x < n ? s_pick[threadIdx.x] : -1, a.E, s_held);
-    for (int e = threadIdx.x; e < a.E; e += threads) s_count[e] = sum_waves(s_held, a.E, e, 0);
+    const int waves = (n + 63) / 64;
+    mine = claim(threadIdx.x < n ? s_pick[threadIdx.x] : -1, a.E, waves, s_held);
+    for (int e = threadIdx.x; e < a.E; e += threads) s_count[e] = sum_waves(s_held, a.E, waves, e, 0);
     __syncthreads();
   } else {
     count_choices(s_pick, n, a.E, s_count);
@@ -329,6 +350,13 @@ __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint
 #pragma unroll
     for (int i = 0; i < PER; ++i) l[i] = on && e0 + i < a.E ? value(row + i) : -INFINITY;
   }
+  float b[WIDE ? PER : 1] = {};                                 // on its way with the logits
+  if constexpr (WIDE) {
+    if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) b[i] = a.bias[min(e0 + i, a.E - 1)];
+    }
+  }
 
   float top = -INFINITY;
 #pragma unroll
@@ -340,24 +368,30 @@ __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint
   Cand<WIDE> v[PER];
   double c[WIDE ? PER : 1];
   if constexpr (WIDE) {
-    double part = 1.0;
-    if (!a.sigmoid) {
+    // (loops without a branch: the experts' 64-bit chains run side by side)
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c[i] = reciprocal64(1.0 + exp64(-static_cast<double>(l[i])));
+    } else {
       double sum = 0.0;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        c[i] = l[i] == -INFINITY ? 0.0 : exp64(static_cast<double>(l[i]) - static_cast<double>(top));
+        const double x = exp64(static_cast<double>(l[i]) - static_cast<double>(top));
+        c[i] = l[i] == -INFINITY ? 0.0 : x;
         sum += c[i];
       }
       sum = across<L>(sum, [](double x, double y) { return x + y; });
-      part = sum > 0.0 ? 1.0 / sum : sum;                      // (no expert at all: 0)
+      const double part = sum > 0.0 ? 1.0 / sum : sum;         // (no expert at all: 0)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c[i] *= part;
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      c[i] = a.sigmoid ? reciprocal64(1.0 + exp64(-static_cast<double>(l[i]))) : c[i] * part;
-      if (a.bias && e0 + i < a.E) c[i] += static_cast<double>(a.bias[e0 + i]);
+      c[i] += static_cast<double>(b[i]);
       const bool live = l[i] != -INFINITY && c[i] != -INFINITY;
-      if (!live) c[i] = -INFINITY;
-      v[i] = {live ? rank64(a.bias ? c[i] : static_cast<double>(l[i])) : 0, static_cast<uint32_t>(e0 + i)};
+      c[i] = live ? c[i] : -INFINITY;
+      const uint64_t rank = rank64(a.bias ? c[i] : static_cast<double>(l[i]));
+      v[i] = {live ? rank : 0, static_cast<uint32_t>(e0 + i)};
     }
   } else {
 #pragma unroll
@@ -417,13 +451,14 @@ __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint
         merge(std::integral_constant<int, 8>{});
         merge(std::integral_constant<int, 16>{});
       }
-      const int mine = sub / a.lanes;
-      int before = 0;
-      for (int g = 0; g < a.groups; ++g) {
-        const uint64_t other = __shfl(key, tk * L + g * a.lanes, 64);
-        before += other > key || (other == key && g < mine);
+      // top_groups times the best of them, of equal ones the lowest: no other of its lanes stands below
+      const uint64_t below = lanes_below<L>(lane & ~(a.lanes - 1));
+      bool kept = false;
+      for (int j = 0; j < a.top_groups; ++j) {
+        const bool here = key == largest<L>(key);
+        if ((__ballot(here) & below) == 0 && here) kept = true, key = 0;
       }
-      if (before >= a.top_groups) {
+      if (!kept) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) v[i].key = 0;
       }
@@ -473,15 +508,16 @@ __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint
   }
 
   sort_descending(v);
+  [[maybe_unused]] const uint64_t below_me = lanes_below<L>(lane);
   uint64_t taken = 0;                                           // the key of choice `sub`
   for (int j = 0; j < a.k; ++j) {
-    const uint64_t best = across<L>(v[0].key, [](uint64_t x, uint64_t y) { return x > y ? x : y; });
+    const uint64_t best = largest<L>(v[0].key);
     if (j == sub) taken = best;
     bool here = best != 0 && v[0].key == best;
     if constexpr (WIDE && L > 1) {
       // the lowest of the lanes that hold it: theirs are the lower experts
-      const uint64_t held = __ballot(here) >> (tk * L);
-      here = here && __ffsll(static_cast<long long>(held)) - 1 == sub;
+      const uint64_t held = __ballot(here);
+      here = here && (held & below_me) == 0;
     }
     if (here) s_pick[j] = v[0].index();
     if (sub == 0 && on && best == 0) s_pick[j] = -1;
@@ -630,6 +666,16 @@ __global__ __launch_bounds__(1024) void k_plan_count(PlanArgs a, int run_tokens,
   plan_run(a, gridDim.x == 1, s_pick, n, static_cast<uint32_t>(first), held, pitch, s_count, s_count + a.E, s_count + 2 * a.E + 1);
 }
 
+// x of this lane and of the lane M further in lanes whose bit M is clear, y in the others
+// (in assembly, and with the wait, as in swap16).
+template <int M>
+__device__ __forceinline__ int32_t give(int32_t x, int32_t y) {
+  static_assert(M == 16 || M == 32, "rows or halves");
+  if constexpr (M == 16) asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+  else asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+  return x + y;
+}
+
 // Many runs: held [runs, pitch] to sums [runs + 1, pitch] over earlier runs; a wave an expert.
 __global__ __launch_bounds__(256) void k_plan_sum(const uint16_t* held, int64_t runs, int pitch, int32_t* sums) {
   const int e = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -646,7 +692,7 @@ __global__ __launch_bounds__(256) void k_plan_sum(const uint16_t* held, int64_t 
 // Workgroups place `each` runs.  With sums they are taken from there; else a workgroup sums
 // the earlier runs' counts and all of them itself: a thread 8 neighbouring experts of every
 // so many runs, then over the lanes and waves.  (8191 tokens, 256 experts: 256 runs, 128 KB of
-// counts for each of 128 workgroups, 7.9 us, a chain of short steps.)
+// counts for each of 128 workgroups, 6.6 us; a third of it the sums, the rest a chain of short steps.)
 // LDS: [pitch] of earlier runs, [pitch] of all, [2][16][pitch] partial sums or [16][E] counts of the
 // waves, and the experts' first rows [E + 1].
 __global__ __launch_bounds__(1024) void k_plan_place(PlanArgs a, int run_tokens, int64_t runs, int each, const uint16_t* held, int pitch,
@@ -667,7 +713,9 @@ __global__ __launch_bounds__(1024) void k_plan_place(PlanArgs a, int run_tokens,
   } else {
     const int columns = pitch / 8, shift = __ffs(columns) - 1, strips = 1024 >> shift;     // (a power of two)
     const int column = threadIdx.x & (columns - 1), strip = threadIdx.x >> shift;
-    int32_t before[8] = {}, total[8] = {};
+    // of this thread's runs: [0] in earlier ones, [1] in all.  Two counts a word are added while they
+    // fit, four runs of at most 8192 choices each.
+    int32_t sum[2][8] = {};
     for (int r0 = strip; r0 < static_cast<int>(runs); r0 += 8 * strips) {
       u32x4_t v[8];                                             // 8 loads on their way at once
 #pragma unroll
@@ -677,53 +725,58 @@ __global__ __launch_bounds__(1024) void k_plan_place(PlanArgs a, int run_tokens,
         if (r < runs) v[b] = *reinterpret_cast<const u32x4_t*>(held + static_cast<int64_t>(r) * pitch + 8 * column);
       }
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        const bool earlier = r0 + b * strips < run0;
+      for (int h = 0; h < 8; h += 4) {
+        if (r0 - strip + h * strips >= static_cast<int>(runs)) break;
+        u32x4_t of[2] = {};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int32_t c = static_cast<int32_t>((v[b][i / 2] >> (16 * (i & 1))) & 0xFFFFu);
-          total[i] += c;
-          before[i] += earlier ? c : 0;
+        for (int b = h; b < h + 4; ++b) {
+          const uint32_t earlier = r0 + b * strips < run0 ? ~0u : 0u;
+          of[0] += v[b] & earlier;
+          of[1] += v[b];
         }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[t][i] += static_cast<int32_t>((of[t][i / 2] >> (16 * (i & 1))) & 0xFFFFu);
       }
     }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    // lanes of a wave with the same column: around the rows of 16, then across them
+    // Lanes of a wave with the same column.  Across the halves a lane adds up one of two values and
+    // leaves the other to its partner: lanes below 32 end with [0], the others with [1]; so again
+    // across the rows of 16, for the values [0, 4) and [4, 8).  Inside a row they turn.
     auto turn = [&](auto by) {
       if (columns > by) return;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        before[i] += lane_move<0x120 + by, 0xF>(before[i]);
-        total[i] += lane_move<0x120 + by, 0xF>(total[i]);
-      }
+      for (int i = 0; i < 4; ++i) sum[0][i] += lane_move<0x120 + by, 0xF>(sum[0][i]);
     };
-    auto cross = [&](auto by) {
-      if (columns > by) return;
+    if (columns <= 32) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t x, y;
-        both<by>(static_cast<uint32_t>(before[i]), x, y);
-        before[i] = static_cast<int32_t>(x + y);
-        both<by>(static_cast<uint32_t>(total[i]), x, y);
-        total[i] = static_cast<int32_t>(x + y);
-      }
-    };
-    turn(std::integral_constant<int, 1>{});
-    turn(std::integral_constant<int, 2>{});
-    turn(std::integral_constant<int, 4>{});
+      for (int i = 0; i < 8; ++i) sum[0][i] = give<32>(sum[0][i], sum[1][i]);
+    }
+    if (columns <= 16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[0][i] = give<16>(sum[0][i], sum[0][4 + i]);
+    }
     turn(std::integral_constant<int, 8>{});
-    cross(std::integral_constant<int, 16>{});
-    cross(std::integral_constant<int, 32>{});
+    turn(std::integral_constant<int, 4>{});
+    turn(std::integral_constant<int, 2>{});
+    turn(std::integral_constant<int, 1>{});
     // waves of the same column: every columns / 64-th, or all
     const int stride = columns > 64 ? columns / 64 : 1, rows = 16 / stride;
-    if (lane < columns) {
-      typedef int i32x4 __attribute__((ext_vector_type(4)));
-      i32x4* part = reinterpret_cast<i32x4*>(s_held + (wave / stride) * pitch + 8 * column);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        part[h] = i32x4{before[4 * h], before[4 * h + 1], before[4 * h + 2], before[4 * h + 3]};
-        part[4 * pitch + h] = i32x4{total[4 * h], total[4 * h + 1], total[4 * h + 2], total[4 * h + 3]};
-      }
+    typedef int i32x4 __attribute__((ext_vector_type(4)));
+    const i32x4 low{sum[0][0], sum[0][1], sum[0][2], sum[0][3]}, high{sum[0][4], sum[0][5], sum[0][6], sum[0][7]};
+    int32_t* part = s_held + (wave / stride) * pitch + 8 * column;
+    if (columns > 32) {
+      *reinterpret_cast<i32x4*>(part) = low;
+      *reinterpret_cast<i32x4*>(part + 4) = high;
+      *reinterpret_cast<i32x4*>(part + 16 * pitch) = i32x4{sum[1][0], sum[1][1], sum[1][2], sum[1][3]};
+      *reinterpret_cast<i32x4*>(part + 16 * pitch + 4) = i32x4{sum[1][4], sum[1][5], sum[1][6], sum[1][7]};
+    } else if (columns == 32) {
+      part += (lane >> 5) * 16 * pitch;
+      *reinterpret_cast<i32x4*>(part) = low;
+      *reinterpret_cast<i32x4*>(part + 4) = high;
+    } else if ((lane & 15) < columns) {
+      *reinterpret_cast<i32x4*>(part + (lane >> 5) * 16 * pitch + (lane >> 4 & 1) * 4) = low;
     }
     __syncthreads();
     for (int e = threadIdx.x; e < 2 * pitch; e += 1024) {       // (s_total follows s_before)
