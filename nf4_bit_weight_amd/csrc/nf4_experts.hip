@@ -40,10 +40,11 @@ __device__ __forceinline__ uint32_t rank32(float x) {
 __device__ __forceinline__ float number32(uint32_t r) {       // and back
   return __builtin_bit_cast(float, r & 0x80000000u ? r & 0x7FFFFFFFu : ~r);
 }
+// (minus infinity is none; x + 0 has no negative zero)
 __device__ __forceinline__ uint64_t rank64(double x) {
-  const uint64_t u = x == 0.0 ? 0u : __builtin_bit_cast(uint64_t, x);
+  const uint64_t u = __builtin_bit_cast(uint64_t, x + 0.0);
   const uint64_t flip = static_cast<uint64_t>(static_cast<int64_t>(u) >> 63) | uint64_t{1} << 63;
-  return x != x ? ~uint64_t{0} : u ^ flip;
+  return x != x ? ~uint64_t{0} : (u ^ flip) - 0x000FFFFFFFFFFFFFu;
 }
 
 // This lane's value and the one of the lane M further in a butterfly over equal
@@ -386,12 +387,13 @@ __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint
       for (int i = 0; i < PER; ++i) c[i] *= part;
     }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      c[i] += static_cast<double>(b[i]);
-      const bool live = l[i] != -INFINITY && c[i] != -INFINITY;
-      c[i] = live ? c[i] : -INFINITY;
-      const uint64_t rank = rank64(a.bias ? c[i] : static_cast<double>(l[i]));
-      v[i] = {live ? rank : 0, static_cast<uint32_t>(e0 + i)};
+    for (int i = 0; i < PER; ++i) c[i] = l[i] == -INFINITY ? -INFINITY : c[i] + static_cast<double>(b[i]);
+    if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = {rank64(c[i]), static_cast<uint32_t>(e0 + i)};
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = {rank64(static_cast<double>(l[i])), static_cast<uint32_t>(e0 + i)};
     }
   } else {
 #pragma unroll
@@ -402,7 +404,7 @@ __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint
   if (a.groups > 1) {
     const int size = a.E / a.groups;
     auto judge = [](double one, double two, bool nan) {
-      return nan ? ~uint64_t{0} : one == -INFINITY ? 0 : rank64(two == -INFINITY ? one : one + two);
+      return nan ? ~uint64_t{0} : rank64(two == -INFINITY ? one : one + two);
     };
     if (a.lanes > 0) {
       // a group is a run of `lanes` lanes, a power of two
@@ -533,36 +535,43 @@ __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint
   // vanish with the scores: softmax from the largest chosen logit, sigmoid (e^l / (1 + e^l)
   // below zero) with all of them scaled up by the best where that is far down.
   const int mine = on ? a.k : 0;
-  auto chosen = [&](int j) {                                    // the logit of a choice
-    const int e = s_pick[j];
-    if (e < 0) return -INFINITY;
-    return !WIDE && j == sub ? number32(static_cast<uint32_t>(taken >> 32)) : value(logits + e);
-  };
-  float best = -INFINITY, total = 0.0f;
+  auto logit = [&](int e) { return e < 0 ? -INFINITY : value(logits + e); };
+  // a lane has choice `sub` in registers; more where there are more than lanes
+  const int first = sub < mine ? s_pick[sub] : -1;
+  const float first_logit = !WIDE && first >= 0 ? number32(static_cast<uint32_t>(taken >> 32)) : logit(first);
+  float best, total;
   if (a.renorm) {
-    for (int j = sub; j < mine; j += L) best = fmaxf(best, chosen(j));
+    best = first_logit;
+    for (int j = sub + L; j < mine; j += L) best = fmaxf(best, logit(s_pick[j]));
     best = across<L>(best, [](float x, float y) { return fmaxf(x, y); });
     if (best == -INFINITY || (a.sigmoid && best > 0.0f)) best = 0.0f;
   } else {
     best = a.sigmoid ? 0.0f : top;
   }
-  auto score = [&](float x) {
+  auto score = [&](int e, float x) {
+    if (e < 0) return 0.0f;
     if (!a.sigmoid) return expf(x - best);
     return x >= 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x - best) / (1.0f + expf(x));
   };
+  const float first_score = score(first, first_logit);
   if (a.renorm) {
-    for (int j = sub; j < mine; j += L) total += s_pick[j] >= 0 ? score(chosen(j)) : 0.0f;
-  } else if (!a.sigmoid) {
+    total = first_score;
+    for (int j = sub + L; j < mine; j += L) total += score(s_pick[j], logit(s_pick[j]));
+  } else {
+    total = 0.0f;
+    if (!a.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) total += exp_from(l[i], top);
+      for (int i = 0; i < PER; ++i) total += exp_from(l[i], top);
+    }
   }
   total = across<L>(total, [](float x, float y) { return x + y; });
   if (a.sigmoid && !a.renorm) total = 1.0f;
-  for (int j = sub; j < mine; j += L) {
-    const int e = s_pick[j];
+  auto write = [&](int j, int e, float s) {
     a.experts[t * a.k + j] = e;
-    a.weights[t * a.k + j] = e >= 0 ? a.scale * (score(chosen(j)) / total) : 0.0f;
-  }
+    a.weights[t * a.k + j] = e >= 0 ? a.scale * (s / total) : 0.0f;
+  };
+  if (sub < mine) write(sub, first, first_score);
+  for (int j = sub + L; j < mine; j += L) write(j, s_pick[j], score(s_pick[j], logit(s_pick[j])));
   if (!plan.offsets) return;
   __syncthreads();
   const int n = static_cast<int>(min(static_cast<int64_t>(waves * kTokens), a.T - t0)) * a.k;
