@@ -102,7 +102,8 @@ __device__ __forceinline__ V across(V v, F f) {
 }
 
 // The largest of the L lanes' values: of the high halves, then of the low halves beside that one.  (Two
-// searches of 32 bits, whose maxima take the lane moves with them, are 24 instructions for the 40 of one of 64.)
+// searches of 32 bits, whose maxima take the lane moves with them: a choice takes 43 vector instructions, 54 with
+// one search of 64.)
 template <int L>
 __device__ __forceinline__ uint64_t largest(uint64_t v) {
   auto most = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
@@ -318,11 +319,12 @@ __device__ __forceinline__ void plan_run(const PlanArgs& a, bool only, const int
 // in 64 bits, since 8191 x 256 scores hold several pairs that fp32 rounding would turn round.
 //
 // A workgroup's tokens are a run of the plan: it counts their choices for k_plan_place, or,
-// as the only one, places them itself (one launch for a batch of new tokens: 4.8 us for one).
+// as the only one, places them itself (one launch for a batch of new tokens: 5.0 us for one).
 //
-// What bounds it: instructions.  8191 tokens, 256 experts, sigmoid with a bias in 8 groups: 15.5 us, 1630
-// vector instructions a wave of two tokens, most of them the 64-bit scores and keys; the bytes take 1.9 us.
-// 16384 tokens, 64 experts, bf16 and softmax: 6.4.
+// What bounds it: instructions.  8191 tokens, 256 experts, sigmoid with a bias in 8 groups: 15.8 us alone,
+// 20.5 with the plan (23.2 at 1630 vector instructions a wave of two tokens; now 1280, a fifth of them the
+// scores in 64 bits, a fourth the choices); the bytes take 1.9 us.  16384 tokens, 64 experts, bf16 and
+// softmax: 6.3.
 template <typename T, int PER, int L, bool WIDE>
 __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint16_t* held, int pitch) {
   constexpr int kTokens = 64 / L, kOf = L * PER;
