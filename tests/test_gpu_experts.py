@@ -207,6 +207,36 @@ def test_plan_of_any_integers():
         assert torch.equal(got.cpu(), want)
 
 
+def sorted_plan(e, E):
+    flat, k = e.flatten().long(), e.shape[1]
+    flat = torch.where((flat < 0) | (flat >= E), E, flat)
+    order, count = flat.argsort(stable=True), flat.bincount(minlength=E + 1)
+    offsets, used = torch.cat([count.new_zeros(1), count[:E].cumsum(0)]), int(count[:E].sum())
+    tokens, slots = torch.full_like(flat, -1), torch.full_like(flat, -1)
+    tokens[:used] = order[:used] // k
+    slots[order[:used]] = torch.arange(used)
+    return offsets.int(), tokens.int(), slots.int().view(e.shape)
+
+
+@pytest.mark.parametrize("T,E,k", [(9000, 2, 1), (9001, 8, 8), (5000, 11, 3), (3000, 32, 4), (1500, 64, 6), (1501, 120, 8), (700, 256, 8),
+                                   (16390, 256, 2), (400, 500, 5), (330, 1000, 3), (5000, 1024, 4), (40000, 600, 1)])
+def test_plan_of_many_runs(T, E, k):
+    """Every width of the counts, from few workgroups' to those that are summed beforehand."""
+    logits = R.normal(T + E, T, E)
+    logits[::7] = -float("inf")
+    r = nf4_route(logits.to(DEV), k)
+    for got, want, plan in zip((r.offsets, r.tokens, r.slots), sorted_plan(r.experts.cpu(), E), nf4_expert_plan(r.experts, E)):
+        assert torch.equal(got.cpu(), want) and torch.equal(plan, got)
+
+
+def test_plan_where_one_expert_takes_all():
+    """Runs of 8192 choices of one expert, several to a thread that adds them up."""
+    e = torch.full((76800, 64), 63, dtype=torch.int32)
+    e[40000:40003] = 62
+    for got, want in zip(nf4_expert_plan(e.to(DEV), 64), sorted_plan(e, 64)):
+        assert torch.equal(got.cpu(), want)
+
+
 def test_route_of_no_tokens():
     r = nf4_route(torch.empty((0, 16), device=DEV), 4)
     assert r.weights.shape == (0, 4) and r.tokens.numel() == 0 and r.offsets.tolist() == [0] * 17
