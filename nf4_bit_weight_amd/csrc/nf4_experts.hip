@@ -321,7 +321,7 @@ __device__ __forceinline__ void plan_run(const PlanArgs& a, bool only, const int
 // A workgroup's tokens are a run of the plan: it counts their choices for k_plan_place, or,
 // as the only one, places them itself (one launch for a batch of new tokens: 5.0 us for one).
 //
-// What bounds it: instructions.  8191 tokens, 256 experts, sigmoid with a bias in 8 groups: 15.8 us alone,
+// What bounds it: instructions.  8191 tokens, 256 experts, sigmoid with a bias in 8 groups: 15.5 us alone,
 // 20.5 with the plan (23.2 at 1630 vector instructions a wave of two tokens; now 1280, a fifth of them the
 // scores in 64 bits, a fourth the choices); the bytes take 1.9 us.  16384 tokens, 64 experts, bf16 and
 // softmax: 6.3.
