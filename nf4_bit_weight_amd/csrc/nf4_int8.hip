@@ -77,10 +77,19 @@ __device__ __forceinline__ uint32_t largest_of(const float (&v)[8], uint32_t top
   for (int e = 0; e < 8; ++e) top_bits = max(top_bits, __builtin_bit_cast(uint32_t, v[e]) & 0x7FFFFFFFu);
   return top_bits;
 }
+// over the 16 lanes of a row, in lane moves of the vector unit (quad_perm twice, row_half_mirror, row_mirror)
+template <int MOVE>
+__device__ __forceinline__ uint32_t moved_max(uint32_t v) {
+  const uint32_t o = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), MOVE, 0xF, 0xF, true));
+  return o > v ? o : v;
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  return moved_max<0x140>(moved_max<0x141>(moved_max<0x4E>(moved_max<0xB1>(v))));
+}
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v = max(v, __shfl_xor(v, m, 64));
-  return v;
+  const int m = static_cast<int>(row_max(v));                  // (below 2^31)
+  return static_cast<uint32_t>(max(max(__builtin_amdgcn_readlane(m, 0), __builtin_amdgcn_readlane(m, 16)),
+                                   max(__builtin_amdgcn_readlane(m, 32), __builtin_amdgcn_readlane(m, 48))));
 }
 struct RowScale {
   float top, inverse, scale;
@@ -525,9 +534,7 @@ __global__ __launch_bounds__(512, EU) void k_stream(Int8Args a, FusedX fx, int m
 #pragma unroll
       for (int j = 0; j < kMost; ++j) {
         if (of[j] < 0) continue;
-        uint32_t top = largest_of(f[j], 0);
-#pragma unroll
-        for (int m = 1; m < 16; m <<= 1) top = max(top, __shfl_xor(top, m, 64));
+        const uint32_t top = row_max(largest_of(f[j], 0));
         if ((lane & 15) == 0) atomicMax(&s_top[of[j]], top);    // (the largest of integers: in any order)
       }
       __syncthreads();
