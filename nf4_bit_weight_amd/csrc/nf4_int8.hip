@@ -288,16 +288,12 @@ __global__ __launch_bounds__(64 * T::kWaves, 1) void k_tile(Int8Args a, int m_ti
     const int r = T::kRows * (wave * IW + i) + lane / kUnits;
     ws[i] = reinterpret_cast<const char*>(a.q) + (rt.e * a.N + min(n0 + r, a.N - 1)) * a.pitch + 16 * unit_at<BK>(r, lane % kUnits);
   }
-  // scales and bias are on their way while the products run: a thread fetches one row's or column's
+  // Scales and bias are on their way while the products run: a thread fetches one row's or column's.
   static_assert(BM + BN <= 64 * T::kWaves, "one scale a thread");
-  float early_scale = 0.0f, early_bias = 0.0f;
-  if (threadIdx.x < BM) {
-    early_scale = a.x_scale[row_of(a, min(rt.first + threadIdx.x, rt.end - 1))];
-  } else if (threadIdx.x < BM + BN) {
-    const int64_t n = min(n0 + threadIdx.x - BM, a.N - 1);
-    early_scale = a.scale[rt.e * a.N + n];
-    if (a.bias) early_bias = a.bias[n];
-  }
+  // Its row's number comes with those of the copies, and the scale itself is asked for behind the first of
+  // them: 512 tokens of 8 of 64 experts 47.0 -> 45.5 us where the copies waited for both.
+  const int tid = static_cast<int>(threadIdx.x);
+  const int64_t scale_row = row_of(a, min(rt.first + min(tid, BM - 1), rt.end - 1)), scale_n = min(n0 + max(tid - BM, 0), a.N - 1);
   const uint32_t base = lds_addr(lds);
   auto copy = [&](uint32_t stage, int i) {                     // i-th of C
     if (i < IX) {
@@ -335,6 +331,8 @@ __global__ __launch_bounds__(64 * T::kWaves, 1) void k_tile(Int8Args a, int m_ti
   for (int k = 0; k < ahead; ++k)
 #pragma unroll
     for (int i = 0; i < C; ++i) copy(k * T::kStage, i);
+  const float early_scale = *(tid < BM ? a.x_scale + scale_row : a.scale + rt.e * a.N + scale_n);
+  const float early_bias = a.bias ? a.bias[scale_n] : 0.0f;
   if (steps > 0) {
     if (steps >= NS - 1) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "n"((NS - 2) * C) : "memory");
     else landed(false);
