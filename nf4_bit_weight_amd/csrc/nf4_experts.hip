@@ -405,7 +405,7 @@ __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint
 
   if (a.groups > 1) {
     const int size = a.E / a.groups;
-    auto judge = [](double one, double two, bool nan) {
+    auto group_rank = [](double one, double two, bool nan) {
       return nan ? ~uint64_t{0} : rank64(two == -INFINITY ? one : one + two);
     };
     if (a.lanes > 0) {
@@ -436,7 +436,7 @@ __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint
         merge(std::integral_constant<int, 4>{});
         merge(std::integral_constant<int, 8>{});
         merge(std::integral_constant<int, 16>{});
-        key = judge(one, two, nan != 0);
+        key = group_rank(one, two, nan != 0);
       } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -488,7 +488,7 @@ __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint
             two = fmax(two, fmin(one, x));
             one = fmax(one, x);
           }
-          key = judge(one, two, nan);
+          key = group_rank(one, two, nan);
         } else {
           for (int i = 0; i < size; ++i) key = s[i] > key ? s[i] : key;
         }

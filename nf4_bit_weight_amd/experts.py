@@ -74,7 +74,7 @@ def nf4_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: Op
     """The top_k of the E experts of each row of logits [T, E], their weights and
     the plan.  Scores are the softmax or the sigmoid of the logits.  `bias` (float32
     [E]) moves the choice towards balance and enters no weight.  With `groups` the
-    experts are chosen inside the top_groups best of so many equal runs, judged by
+    experts are chosen inside the top_groups best of so many equal runs, ranked by
     their best ("max") or their best two together ("top2").  Weights are the
     chosen scores, divided by their sum with `renormalize`, times `scale`.  An expert
     whose logit is -inf is never chosen; where fewer than top_k are left the

@@ -39,7 +39,7 @@ def choose(l, k, score="softmax", bias=None, groups=1, top_groups=1, group_score
     allowed = range(len(l))
     if groups > 1:
         size = len(l) // groups
-        judged = []
+        rated = []
         for g in range(groups):
             mine = range(g * size, (g + 1) * size)
             best = sorted((c[i] for i in mine if c[i] is not None), reverse=True)
@@ -47,8 +47,8 @@ def choose(l, k, score="softmax", bias=None, groups=1, top_groups=1, group_score
                 by = max((order[i] for i in mine if order[i] is not None), default=None)
             else:
                 by = sum(best[:2]) if best else None
-            judged.append((-math.inf if by is None else by, -g, by is not None))
-        kept = sorted(judged, reverse=True)[:top_groups]
+            rated.append((-math.inf if by is None else by, -g, by is not None))
+        kept = sorted(rated, reverse=True)[:top_groups]
         allowed = [i for _, g, some in kept if some for i in range(-g * size, (-g + 1) * size)]
     ranked = sorted((i for i in allowed if order[i] is not None), key=lambda i: (-order[i], i))[:k]
     return ranked + [-1] * (k - len(ranked))

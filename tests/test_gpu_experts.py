@@ -46,11 +46,11 @@ def test_route_shapes(T, E, k, dtype):
 @pytest.mark.parametrize("T,E,k,groups,top", [(37, 64, 8, 8, 4), (5, 256, 8, 8, 4), (11, 256, 6, 16, 3), (9, 60, 4, 4, 2), (4, 8, 2, 8, 2),
                                               (3, 16, 2, 2, 1), (2, 1024, 8, 64, 8), (6, 120, 3, 40, 5), (7, 33, 3, 11, 11),
                                               (2, 900, 20, 3, 2), (3, 64, 8, 64, 20)])
-@pytest.mark.parametrize("judge", ["max", "top2"])
-def test_route_groups(T, E, k, groups, top, judge):
+@pytest.mark.parametrize("rank", ["max", "top2"])
+def test_route_groups(T, E, k, groups, top, rank):
     l = R.normal(E + groups, T, E)
     for score, bias in itertools.product(("softmax", "sigmoid"), (None, 0.05 * R.normal(3, E))):
-        check_route(l, k, score=score, bias=bias, groups=groups, top_groups=top, group_score=judge, renormalize=True)
+        check_route(l, k, score=score, bias=bias, groups=groups, top_groups=top, group_score=rank, renormalize=True)
 
 
 @pytest.mark.parametrize("E", [8, 64, 300])
