@@ -156,11 +156,12 @@ __device__ __forceinline__ void sort_descending(Cand<WIDE> (&v)[PER]) {
         }
 }
 
-// e^x in 64 bits: x = n ln 2 + r, the series of e^r to its 13th term (the next is below
-// 2^-57 at |r| = ln 2 / 2), times 2^n.  Half of what the library's takes, which
-// serves the ends of the range; here they are cut off at +-700.
+// e^x for x <= 0 in 64 bits: x = n ln 2 + r, the series of e^r to its 13th term (the next is
+// below 2^-57 at |r| = ln 2 / 2), times 2^n, which goes down to the smallest number above zero
+// (e^-745.1): scores that differ in 64 bits stay different.  Half of what the library's takes,
+// which serves large x too.
 __device__ __forceinline__ double exp64(double x) {
-  const double y = fmin(fmax(x, -700.0), 700.0);
+  const double y = fmax(x, -746.0);                             // zero from here on; n stays an integer
   const double n = rint(y * 1.4426950408889634074);
   double r = fma(-n, 0.69314718055994530942, y);
   r = fma(-n, 2.3190468138462995e-17, r);                      // ln 2 less its 64-bit value
@@ -180,7 +181,7 @@ __device__ __forceinline__ double exp64(double x) {
   p = fma(p, r, 1.0);
   return x != x ? x : ldexp(p, static_cast<int>(n));
 }
-// 1 / x for 1 <= x < 2^1012: the hardware's guess, made good twice
+// 1 / x for 1 <= x <= 2: the hardware's guess, made good twice
 __device__ __forceinline__ double reciprocal64(double x) {
   double r = __builtin_amdgcn_rcp(x);
   r = fma(fma(-x, r, 1.0), r, r);
@@ -374,7 +375,11 @@ __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint
     // (loops without a branch: the experts' 64-bit chains run side by side)
     if (a.sigmoid) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) c[i] = reciprocal64(1.0 + exp64(-static_cast<double>(l[i])));
+      for (int i = 0; i < PER; ++i) {
+        // e^-|l| either way: nothing overflows, and below zero the score is as small as e^l
+        const double x = exp64(-static_cast<double>(fabsf(l[i]))), r = reciprocal64(1.0 + x);
+        c[i] = l[i] < 0.0f ? x * r : r;
+      }
     } else {
       double sum = 0.0;
 #pragma unroll
