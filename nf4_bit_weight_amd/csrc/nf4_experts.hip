@@ -1029,19 +1029,9 @@ int run_waves(int32_t E, int32_t k) {
 
 size_t plan_lds(int32_t E, int waves) { return static_cast<size_t>(2 * E + 1 + waves * E) * 4; }
 
-template <typename K>
-void allow_lds(K kernel) {
-  (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-  (void)hipGetLastError();
-}
-
 // The second half, behind the counts.
 hipError_t launch_place(const PlanArgs& a, const Runs& r, uint16_t* held, hipStream_t stream) {
-  static const bool done = [] {
-    allow_lds(k_plan_place);
-    return true;
-  }();
-  (void)done;
+  allow_lds<k_plan_place>();
   int32_t* sums = nullptr;
   if (r.each == 0) {
     sums = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(held) + r.held_bytes);
@@ -1072,16 +1062,13 @@ hipError_t launch_route(const RouteArgs& args, const PlanArgs& plan, void* ws, h
   const hipError_t e = with_lanes(a.E, [&](auto per_c, auto lanes_c) {
     constexpr int PER = per_c, L = lanes_c;
     auto go = [&](auto kernel) {
-      static const bool done = [&] {
-        allow_lds(kernel);
-        return true;
-      }();
-      (void)done;
-      kernel<<<static_cast<uint32_t>(r.runs), 64 * r.waves, bytes, stream>>>(a, plan, held, r.pitch);
+      constexpr auto launch = decltype(kernel)::launch;
+      allow_lds<launch>();
+      launch<<<static_cast<uint32_t>(r.runs), 64 * r.waves, bytes, stream>>>(a, plan, held, r.pitch);
       return hipGetLastError();
     };
-    if (a.bf16) return wide ? go(k_route<uint16_t, PER, L, true>) : go(k_route<uint16_t, PER, L, false>);
-    return wide ? go(k_route<float, PER, L, true>) : go(k_route<float, PER, L, false>);
+    if (a.bf16) return wide ? go(Kernel<k_route<uint16_t, PER, L, true>>{}) : go(Kernel<k_route<uint16_t, PER, L, false>>{});
+    return wide ? go(Kernel<k_route<float, PER, L, true>>{}) : go(Kernel<k_route<float, PER, L, false>>{});
   });
   if (e != hipSuccess || !plan.offsets || r.runs == 1) return e;
   return launch_place(plan, r, held, stream);
@@ -1108,11 +1095,7 @@ hipError_t launch_plan(const PlanArgs& a, void* ws, hipStream_t stream) {
   const Runs r = runs_of(a.T, a.E, waves_for(a.T, a.E, run_waves(a.E, a.k)));
   uint16_t* held = static_cast<uint16_t*>(ws);
   const size_t lds = static_cast<size_t>(r.tokens) * a.k * 4 + plan_lds(a.E, r.runs == 1 ? 16 : 0);
-  static const bool done = [] {
-    allow_lds(k_plan_count);
-    return true;
-  }();
-  (void)done;
+  allow_lds<k_plan_count>();
   k_plan_count<<<static_cast<uint32_t>(r.runs), 1024, lds, stream>>>(a, r.tokens, held, r.pitch);
   if (r.runs == 1) return hipGetLastError();
   const hipError_t e = hipGetLastError();

@@ -614,18 +614,14 @@ hipError_t launch_stream(const Int8Args& a, const FusedX* fx, hipStream_t stream
   const int64_t m_tiles = row_tiles(a, 16 * MT), cols = 8 / kw * 16 * NT, n_tiles = (a.N + cols - 1) / cols;
   const size_t held = fx ? (a.x_rows * (a.pitch + 20) + 15) / 16 * 16 : 0, bytes = held + (kw > 1 ? 8 * MT * NT * 1024 : 0);
   auto go = [&](auto kernel) {
-    static const bool done = [&] {
-      (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-      (void)hipGetLastError();
-      return true;
-    }();
-    (void)done;
-    kernel<<<static_cast<uint32_t>(m_tiles * n_tiles), 512, bytes, stream>>>(a, fx ? *fx : FusedX{}, static_cast<int>(m_tiles),
+    constexpr auto launch = decltype(kernel)::launch;
+    allow_lds<launch>();
+    launch<<<static_cast<uint32_t>(m_tiles * n_tiles), 512, bytes, stream>>>(a, fx ? *fx : FusedX{}, static_cast<int>(m_tiles),
                                                                               static_cast<int>(n_tiles), kw);
     return hipGetLastError();
   };
-  if (fx) return a.bf16 ? go(k_stream<MT, NT, U, EU, true, uint16_t>) : go(k_stream<MT, NT, U, EU, true, float>);
-  return a.bf16 ? go(k_stream<MT, NT, U, EU, false, uint16_t>) : go(k_stream<MT, NT, U, EU, false, float>);
+  if (fx) return a.bf16 ? go(Kernel<k_stream<MT, NT, U, EU, true, uint16_t>>{}) : go(Kernel<k_stream<MT, NT, U, EU, true, float>>{});
+  return a.bf16 ? go(Kernel<k_stream<MT, NT, U, EU, false, uint16_t>>{}) : go(Kernel<k_stream<MT, NT, U, EU, false, float>>{});
 }
 
 template <typename T>
@@ -634,16 +630,12 @@ hipError_t launch_tile(const Int8Args& a, hipStream_t stream) {
   const int64_t n_tiles = (a.N + T::BN - 1) / T::BN;
   if (a.offsets) m_tiles = (m_tiles + 7) / 8 * 8;
   auto go = [&](auto kernel) {
-    static const bool done = [&] {
-      (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, T::kBytes);
-      (void)hipGetLastError();
-      return true;
-    }();
-    (void)done;
-    kernel<<<static_cast<uint32_t>(m_tiles * n_tiles), 64 * T::kWaves, T::kBytes, stream>>>(a, static_cast<int>(m_tiles), static_cast<int>(n_tiles));
+    constexpr auto launch = decltype(kernel)::launch;
+    allow_lds<launch>();
+    launch<<<static_cast<uint32_t>(m_tiles * n_tiles), 64 * T::kWaves, T::kBytes, stream>>>(a, static_cast<int>(m_tiles), static_cast<int>(n_tiles));
     return hipGetLastError();
   };
-  return a.bf16 ? go(k_tile<T, uint16_t>) : go(k_tile<T, float>);
+  return a.bf16 ? go(Kernel<k_tile<T, uint16_t>>{}) : go(Kernel<k_tile<T, float>>{});
 }
 
 }  // namespace

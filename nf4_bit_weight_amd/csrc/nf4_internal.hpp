@@ -74,6 +74,24 @@ hipError_t launch_gemm8(GemmKind kind, const GemmPlan& plan, const void* A, int6
 hipError_t launch_grouped8(GemmKind kind, const void* A, const int32_t* offsets, int32_t E,
                            int64_t total_M, const WArgs& w, void* C, hipStream_t stream);
 
+// A kernel as a type, so that generic code keeps what belongs to it apart from
+// others of the same signature.
+template <auto F>
+struct Kernel {
+  static constexpr auto launch = F;
+};
+// Raises F's limit on dynamic LDS to all that a compute unit has, before its first
+// launch (thread-safe static initialisation); a failure here surfaces at the launch.
+template <auto F>
+void allow_lds() {
+  static const bool done = [] {
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(F), hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    (void)hipGetLastError();
+    return true;
+  }();
+  (void)done;
+}
+
 // path counters (defined in nf4_abi.hip)
 void count_path(int path);
 
