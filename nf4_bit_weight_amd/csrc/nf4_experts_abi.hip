@@ -21,7 +21,8 @@ bool is_float(int dtype) { return dtype == NF4_DTYPE_F32 || dtype == NF4_DTYPE_B
 int check_choices(int64_t T, int32_t E, int32_t k) {
   if (T < 0 || E < 1 || k < 1 || k > E) return NF4_ERR_SHAPE;
   if (E > 1024 || k > 64 || T > (1 << 30) / k) return NF4_ERR_UNSUPPORTED;
-  return launchable(T, 64) ? NF4_OK : NF4_ERR_UNSUPPORTED;     // a wave a token at most
+  // above 256 experts a wave a token, up to 16 waves a workgroup (which the last one fills up)
+  return launchable(E > 256 ? (T + 15) / 16 * 16 : T, 64) ? NF4_OK : NF4_ERR_UNSUPPORTED;
 }
 
 // Rows of the tokens and of their choices.

@@ -49,6 +49,12 @@ def matmul(M, N, K, dt, out):
     return lib.nf4_int8_matmul(A, dt, K, A, M, A, A, N, K, None, A, out, A, BIG, None)
 def grouped(M, N, K, E, dt, out):
     return lib.nf4_int8_grouped_matmul(A, dt, K, A, M, None, A, E, M, A, A, N, K, A, out, 1, A, BIG, None)
+def rows(f, T, H, k, dt):
+    a = {"gather": (A, dt, H, T, H, k, A, A, A, 1), "gather_bwd": (A, dt, T, H, k, A, A), "combine_fwd": (A, dt, T, H, k, A, A, A),
+         "combine_bwd": (A, H, A, dt, T, H, k, A, A, A, A, A, 1)}[f]
+    return getattr(lib, "nf4_expert_" + f)(*a, None)
+def quantize(M, K, dt):
+    return lib.nf4_int8_quantize(A, dt, K, M, K, A, A, None)
 for line in sys.stdin:
     say("call " + line.strip())
     say("status %d" % eval(line))
@@ -116,3 +122,13 @@ def test_every_kernel_may_have_its_lds(watch, backwards):
     for kind, many in (("k_route", 16), ("k_tile", 12), ("k_stream", 12)):
         assert sum(kind in n and not "bwd" in n for n in kernels) >= many, (kind, sorted(kernels))
     assert sum(lds > 65536 for lds in kernels.values()) >= 16
+
+
+def test_sizes_that_fit_are_taken(watch):
+    """The refusals stay close to what a launch holds."""
+    calls = [f"route({(1 << 26) - 1}, 256, 8, 1, 1, {BF16})", f"route({(1 << 26) - 16}, 1024, 1, 1, 1, {BF16})",
+             f"route({(1 << 26) - 16}, 513, 1, 3, 1, {BF16})", f"route_bwd({(1 << 26) - 16}, 1024, 1, {BF16})", f"plan({(1 << 26) - 16}, 1024, 1)"]
+    assert [status for _, status, _ in watch(calls)] == [0] * len(calls)
+    refused = [f"route({(1 << 26) - 15}, 257, 1, 1, 1, {BF16})", f"route_bwd({(1 << 26) - 1}, 1024, 1, {BF16})", f"plan({(1 << 26) - 1}, 1024, 1)",
+               f"route({1 << 26}, 64, 1, 1, 1, {BF16})"]
+    assert [(status, launches) for _, status, launches in watch(refused)] == [(L.NF4_ERR_UNSUPPORTED, [])] * len(refused)
