@@ -1037,7 +1037,8 @@ hipError_t launch_place(const PlanArgs& a, const Runs& r, uint16_t* held, hipStr
     sums = reinterpret_cast<int32_t*>(reinterpret_cast<char*>(held) + r.held_bytes);
     k_plan_sum<<<r.pitch / 4, 256, 0, stream>>>(held, r.runs, r.pitch, sums);
   }
-  const int64_t each = r.each == 0 ? 1 : r.each;
+  // (runs of four tokens, of groups that go through LDS, can be more than a launch holds workgroups of 1024)
+  const int64_t each = r.each == 0 ? (r.runs >> 21) + 1 : r.each;
   const size_t behind = static_cast<size_t>(r.each == 0 ? 16 * a.E : 32 * r.pitch), lds = (2 * r.pitch + a.E + 1 + behind) * 4;
   k_plan_place<<<static_cast<uint32_t>((r.runs + each - 1) / each), 1024, lds, stream>>>(a, r.tokens, r.runs, static_cast<int>(each), held,
                                                                                         r.pitch, sums);

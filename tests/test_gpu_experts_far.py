@@ -1,4 +1,4 @@
-"""The choice of experts where scores leave the normal range of 64 bits: far
+"""The choice of experts at its ends.  Where scores leave the normal range of 64 bits: far
 below zero (sigmoid) or far below the largest logit (softmax) they differ by
 powers of two down to 2^-1074, and the order is that of the numbers there too."""
 
@@ -82,3 +82,22 @@ def test_scores_around_zero_keep_their_order_under_a_bias():
     check_choice(l, 40, score="sigmoid", bias=torch.zeros(E))
     check_choice(l, 40, score="sigmoid", bias=torch.full((E,), 0.125))
     assert math.exp(-745.0) > 0.0                                # what the plain form counts on
+
+
+def test_plan_of_more_runs_than_workgroups():
+    """Groups of odd size take runs of four tokens; above 2^21 of those a workgroup places several."""
+    T, E = (1 << 23) + 5, 260
+    l = torch.randn((T, E), device=DEV, dtype=torch.bfloat16, generator=torch.Generator(DEV).manual_seed(5))
+    l[::1000] = -math.inf
+    r = nf4_route(l, 1, groups=13, top_groups=2)
+    best = torch.where(torch.isinf(l[:, 0]), -1, l.argmax(-1)).int()
+    assert torch.equal(torch.where(r.experts[:, 0] >= 0, l.gather(1, r.experts.clamp(min=0).long())[:, 0], 0), torch.where(best >= 0, l.amax(-1), 0))
+    assert torch.equal(r.experts[:, 0] < 0, best < 0)
+    key = torch.where(r.experts[:, 0] < 0, E, r.experts[:, 0]).long()
+    order, count = key.sort(stable=True).indices, torch.bincount(key, minlength=E + 1)
+    assert torch.equal(r.offsets[1:].long(), count[:E].cumsum(0)) and int(r.offsets[0]) == 0
+    used = int(r.offsets[-1])
+    assert torch.equal(r.tokens[:used].long(), order[:used]) and bool((r.tokens[used:] == -1).all())
+    slots = torch.full((T,), -1, device=DEV, dtype=torch.long)
+    slots[order[:used]] = torch.arange(used, device=DEV)
+    assert torch.equal(r.slots[:, 0].long(), slots)

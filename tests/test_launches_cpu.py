@@ -124,6 +124,37 @@ def test_every_kernel_may_have_its_lds(watch, backwards):
     assert sum(lds > 65536 for lds in kernels.values()) >= 16
 
 
+def sizes_at_the_limits():
+    calls = []
+    for E in (1, 8, 64, 100, 256, 257, 512, 513, 1024):
+        for k in (1, 8, 64):
+            for T in sorted({(1 << 30) // k, (1 << 26) - 1, (1 << 26) - 15, (1 << 26) - 16, 1 << 25, 1 << 24, (1 << 24) - 1} if k <= 16 else {(1 << 30) // k}):
+                calls.append(f"plan({T}, {E}, {k})")
+                if k > E:
+                    continue
+                calls += [f"route({T}, {E}, {k}, 1, 1, {BF16})", f"route({T}, {E}, {k}, 1, 1, {F32}, A)", f"route_bwd({T}, {E}, {k}, {F32})"]
+                calls += [f"route({T}, {E}, {k}, {g}, 1, {F32}, A, 1)" for g in (2, 3) if E % g == 0]
+    for T, H in ((1, 1 << 23), ((1 << 24) - 1, 256), ((1 << 24) - 1, 0), ((1 << 23) - 1, 512), (511, 1 << 23), (65536, 65535)):
+        calls += [f"rows('{f}', {T}, {H}, {k}, {dt})" for f in ("gather", "gather_bwd", "combine_fwd", "combine_bwd") for k in (1, 64) for dt in (F32, BF16)]
+    for M in (1, 16, 17, 64, 65, 1 << 20, (1 << 24) - 1, 1 << 28):
+        calls.append(f"quantize({M}, 5000, {BF16})")
+        for N in (64, 8191, 8192, 1 << 20, 59652288, 1 << 28):
+            for K in (100, 300, 4096):
+                calls += [f"matmul({M}, {N}, {K}, {dt}, 0)" for dt in (BF16, I8)] + [f"grouped({M}, {N}, {K}, {E}, 1, 1)" for E in (1, 1024)]
+    return calls
+
+
+def test_what_a_call_accepts_can_be_launched(watch):
+    """Fewer than 2^32 threads in every launch, or the call is refused before the first of them."""
+    accepted = 0
+    for call, status, launches in watch(sizes_at_the_limits()):
+        assert status == 0 if launches else status in (L.NF4_OK, L.NF4_ERR_UNSUPPORTED, L.NF4_ERR_WORKSPACE), call
+        accepted += status == 0
+        for name, lds, limit, groups, threads in launches:
+            assert 0 < groups < 2 ** 31 and groups * threads < 2 ** 32 and lds <= limit, f"{call}: {name} {groups} x {threads}"
+    assert accepted > 300
+
+
 def test_sizes_that_fit_are_taken(watch):
     """The refusals stay close to what a launch holds."""
     calls = [f"route({(1 << 26) - 1}, 256, 8, 1, 1, {BF16})", f"route({(1 << 26) - 16}, 1024, 1, 1, 1, {BF16})",
