@@ -70,7 +70,8 @@ int nf4_int8_matmul(const void* x, int x_dtype, int64_t stride, const float* x_s
  *            but no access out of range
  *   q, scale the stack [E, N, K] quantised as E*N rows
  * Rows behind offsets[E] are written as zeros where fill_outside is 1 and left as
- * they were where it is 0; their tokens are not read.
+ * they were where it is 0; their tokens are not read.  (Without tokens such rows of x are
+ * quantised with the others; no result depends on them.)
  *   ws       nf4_int8_workspace(x_dtype, x_rows, total_M, N, K, E) bytes
  */
 int nf4_int8_grouped_matmul(const void* x, int x_dtype, int64_t stride,

@@ -322,9 +322,11 @@ __device__ __forceinline__ void plan_run(const PlanArgs& a, bool only, const int
 // A workgroup's tokens are a run of the plan: it counts their choices for k_plan_place, or,
 // as the only one, places them itself (one launch for a batch of new tokens: 5.0 us for one).
 //
-// What bounds it: instructions.  8191 tokens, 256 experts, sigmoid with a bias in 8 groups: 15.5 us alone,
-// 20.5 with the plan (23.2 at 1630 vector instructions a wave of two tokens; now 1280, a fifth of them the
-// scores in 64 bits, a fourth the choices); the bytes take 1.9 us.  16384 tokens, 64 experts, bf16 and
+// What bounds it: 8191 tokens, 256 experts, sigmoid with a bias in 8 groups: 15.7 us alone, 20.7 with the
+// plan (23.2 at 1630 vector instructions a wave of two tokens; now 1300, a fifth of them the scores in 64
+// bits, a fourth the choices); the bytes take 1.9 us.  Their issue is two thirds of it (20.8k cycles of the
+// 32.4k that a compute unit is busy); for the rest one chain of load, scores, sort and choices lies open, since
+// all 4096 waves start together, four a SIMD.  16384 tokens, 64 experts, bf16 and
 // softmax: 6.3.
 template <typename T, int PER, int L, bool WIDE>
 __global__ __launch_bounds__(1024) void k_route(RouteArgs a, PlanArgs plan, uint16_t* held, int pitch) {
@@ -818,7 +820,8 @@ __global__ __launch_bounds__(1024) void k_plan_place(PlanArgs a, int run_tokens,
 
 // ---- rows --------------------------------------------------------------------------
 
-// N values of a row as one load: 16 bytes where rows and pointers allow it, else one value.
+// N values of a row as one load: 16 bytes where rows and pointers allow it, else one value.  (4096 x 8 in
+// bf16 of 2047 beside 2048: gather 34 us for 24, combine 91 for 30, its gradients 110 for 52.)
 template <typename T, int N>
 struct Vec {
   float f[N];

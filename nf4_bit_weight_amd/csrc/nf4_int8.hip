@@ -116,8 +116,9 @@ __device__ __forceinline__ u32x2_t round8(const float (&v)[8], const RowScale& s
 
 // A workgroup a row.  Up to 2048 J elements stay in registers between the search
 // for the largest and the rounding; J = 0 reads the row twice.
-// (2048 x 5120 bf16, 31 MB: 20.4 us with one element a load, 11.1 to 12.4 so; at a copy's rate the
-// bytes take 6.2.)
+// (2048 x 5120 bf16, 31 MB: 20.4 us with one element a load, 10.1 to 12.4 so; at a copy's rate the
+// bytes take 6.2.  All those rows are in work at once, and each is read whole, waited for, and only
+// then written, so that little reading and writing overlaps.)
 template <typename T, int J, bool VEC>
 __global__ __launch_bounds__(256) void k_quantize(const T* x, int64_t stride, int K, int pitch, int8_t* q, float* scale) {
   __shared__ uint32_t s_top[4];
@@ -241,7 +242,9 @@ struct Tile {
 // What bounds it: 2048 x 27648 x 5120 in 256 x 256 takes 295 us, 1963 TOP/s (a library product of
 // the same integers, without scales, 306); the matrix units are busy 48 % of the time at the 1.9 GHz that
 // they leave the card under this load.  512 tokens of 8 of 64 experts, 1024 x 2048 each, in 64 x 64: 41 us, of which the bytes
-// take 29; there a wave's products are too few to hide its reads of LDS.
+// would take 29.  Neither they (114 MB moved, 2.8 TB/s) nor the matrix units (busy 12 %) bound it but
+// the tiles: the experts hold 4 to 251 rows, 36 of their 100 row tiles read a weight again and 37 hold at
+// most 32 rows, and 1600 workgroups on 512 places are three rounds and an eighth of one.
 template <typename T, typename Y>
 __global__ __launch_bounds__(64 * T::kWaves, 1) void k_tile(Int8Args a, int m_tiles, int n_tiles) {
   constexpr int BM = T::BM, BN = T::BN, MI = T::MI, NI = T::NI, IX = T::IX, IW = T::IW;
@@ -665,12 +668,14 @@ using Tile256 = Tile<256, 256, 2, 4, 64, 5>;
 
 // Which kernel takes the call, by the rounds of its tiles over the chip and what a
 // round costs (a.pitch counts for all of them alike).  Costs of a round beside each other, from
-// 4096-wide x on one card:
-//   64 x 64      13   256 x 4096   12.7 us    128 x 128   33   1024 x 4096  24.5 us
-//   128 x 64     20   512 x 4096   16.4 us    256 x 128   63   2048 x 4096  42.5 us
-//   256 x 256    96   4096 x 4096  65 us (2100 TOP/s; 110 us in 128 x 128, 90 in 256 x 128)
-// Small sizes keep the chip busy only in small tiles (512 x 4096: 128 x 64 16.4 us, 128 x
-// 128 21, 256 x 256 45), large ones reread too much in them.  Grouped calls do not know their
+// 4096-wide x on one card, with its quantising; behind them the products alone, later:
+//   64 x 64      13   256 x 4096   12.7 us  11.1    128 x 128   33   1024 x 4096  24.5 us  21.3
+//   128 x 64     20   512 x 4096   16.4 us  14.7    256 x 128   63   2048 x 4096  42.5 us  40.9
+//   256 x 256    96   4096 x 4096  65 us  62.4 (2200 TOP/s; 94 us in 128 x 128, 82 in 256 x 128)
+// Small sizes keep the chip busy only in small tiles (512 x 4096: 128 x 64 14.7 us, 128 x
+// 128 16.5, 256 x 256 41), large ones reread too much in them.  No choice cuts the contraction: from
+// 65 rows on a product of few channels leaves most of the chip idle (128 x 1024 x 4096: 32 workgroups, 9.5 us;
+// 128 x 4096 x 14336: 128 of them, 25.5 us, of which the bytes take 12.7).  Grouped calls do not know their
 // tiles here: a part of a tile is lost for every expert.  Their costs are of rounds of experts' tiles,
 // which read other weights each: 512 tokens of 2 of 8 experts 14336 wide take 146 us in 128 x 128, 166 in
 // the 64 x 64 that the costs of the plain product choose.
@@ -698,9 +703,12 @@ int best_shape(const Int8Args& a, int cus) {
 }
 
 // The few-row kernel reads its weights once for 16 or 32 rows, straight from memory, and cuts K
-// eight ways: it takes up to 16 rows (1 x 4096 x 4096: 6.1 us for 13.0 in tiles), and up to 64
-// where tiles would fill less than half of the chip (32 x 4096 x 4096: 9.4 for 12.9; 64 x
-// 1024 x 4096: 6.5 for 9.5; not 32 x 14336 x 4096: 17.6 for 15.4).
+// eight ways: it takes up to 16 rows (1 x 4096 x 4096: 6.2 us for 9.5 in tiles, without quantising), and
+// up to 64 where tiles would fill less than half of the chip (32 x 4096 x 4096: 8.4 for 9.7; 64 x 1024 x
+// 4096: 6.4 for 9.4, x 14336: 15.4 for 25.2; 64 x 2048 x 4096: 8.4 for 9.6; not 32 x 14336 x 4096: 17.7 for
+// 11.7).  Where this is not the faster one: above 32 rows, whose weights it reads twice, from 4096 channels on
+// (64 x 4096 x 4096: 12.4 for 9.9, 64 x 8000 x 4096: 19.6 for 10.0), and in the largest products (16 x 14336 x 4096:
+// 12.6 for 11.4, 32 x 5120 x 27648: 76.9 for 60.9).
 bool few_rows(const Int8Args& a, int cus) {
   if (a.offsets) return false;
   return a.M <= 16 || (a.M <= 64 && (a.N + 63) / 64 < cus / 2);
@@ -725,7 +733,7 @@ hipError_t launch_few_rows(const Int8Args& a, const FusedX* fx, int cus, hipStre
 }  // namespace
 
 // One launch pays while the x that every workgroup quantises for itself is small: one
-// row (1 x 4096 x 4096: 7.5 us for 9.7 in two), or two of 4096 (8.6 for 9.7; four: 11.0 for 10.0).
+// row (1 x 4096 x 4096: 6.8 us for 9.7 in two), or two of 4096 (7.7 for 9.7; four: 11.0 for 9.7).
 bool int8_fused(const Int8Args& a) {
   if (a.pitch == 0 || a.x_rows * a.pitch > (a.x_rows == 1 ? kFusedBytes : kFusedBytes / 2)) return false;
   return few_rows(a, device_cu_count());

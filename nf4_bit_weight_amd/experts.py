@@ -25,8 +25,10 @@ before the capture.
     h = nf4_grouped_linear(rows, r.offsets, w_up, E)            # or nf4_int8_grouped_matmul
     y = nf4_expert_combine(nf4_grouped_linear(act(h), r.offsets, w_down, E), r)
 
-The grouped calls in 4 and 8 bits write no row behind offsets[E]; none of the calls here
-reads one.
+None of the calls here reads a row behind offsets[E].  The grouped calls of `api` and
+`autograd` write none; nf4_int8_grouped_matmul writes zeros there in a result that it
+allocates, and without `tokens` it quantises such rows of x with the others, which no
+result sees.
 """
 
 from __future__ import annotations
@@ -46,7 +48,9 @@ _GROUP_SCORES = {"max": False, "top2": True}
 class NF4Routing:
     """A choice of k experts for each of T tokens, and its plan (nf4_experts.h).
     Rows are the T * k rows that the experts take, sorted by expert and inside
-    one by token; those behind offsets[E] belong to nobody."""
+    one by token; those behind offsets[E] belong to nobody.  The four integer results
+    of nf4_route share one allocation of (3 T k + E + 1) numbers, which lives (and is saved
+    by torch.save) as long as any of them: keep a clone() of one that is to outlive the rest."""
     weights: torch.Tensor      # float32 [T, k]
     experts: torch.Tensor      # int32   [T, k], -1: none
     offsets: torch.Tensor      # int32   [E + 1], as the grouped calls take them
