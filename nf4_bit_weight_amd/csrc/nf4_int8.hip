@@ -668,7 +668,7 @@ using Tile256 = Tile<256, 256, 2, 4, 64, 5>;
 
 // Which kernel takes the call, by the rounds of its tiles over the chip and what a
 // round costs (a.pitch counts for all of them alike).  Costs of a round beside each other, from
-// 4096-wide x on one card, with its quantising; behind them the products alone, later:
+// 4096-wide x on one card, with its quantising; behind them the products alone, on another card:
 //   64 x 64      13   256 x 4096   12.7 us  11.1    128 x 128   33   1024 x 4096  24.5 us  21.3
 //   128 x 64     20   512 x 4096   16.4 us  14.7    256 x 128   63   2048 x 4096  42.5 us  40.9
 //   256 x 256    96   4096 x 4096  65 us  62.4 (2200 TOP/s; 94 us in 128 x 128, 82 in 256 x 128)
